@@ -259,3 +259,9 @@ def workspace(dims, device="cuda"):
     if n == 0:
         raise StrataError(STRATA_ERR_INVALID_ARG, "workspace")
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+from . import kv as _kv  # noqa: E402  (the binding of strata_kv.h uses the helpers above)
+from .kv import *  # noqa: E402,F401,F403
+
+__all__ += _kv.__all__
