@@ -6,9 +6,11 @@ exactly.  A read is exact up to the rounding to bf16 (none in bf16's normal
 range).  Attention, per value, with A = sum_j p_j |v_j| / sum p:
   * the output's rounding, half a bf16 step: 2^-8 |o|;
   * the weights' rounding for the product with V, 2^-9, before it to fp16,
-    2^-11, and their floor of 2^-19 of the tile's largest weight, which over
-    128 positions adds at most 2^-12 of the largest |V| value times 2 (codes
-    reach 448 of a scale whose row may hold only 224);
+    2^-11, and their floor: a tile's largest weight is scaled to 224 .. 448,
+    e4m3's smallest step is 2^-9, so a weight is off by 2^-10 / 224 = 2^-17.8 of the
+    tile's largest at most, in units of the tile's largest V scale, whose codes
+    reach 448 where its row may hold 224: over 128 positions 2^-9.8 of the largest
+    |V| value;
   * the scores: q is split into two e4m3 values, exact down to 2^-17 of the
     row's largest, and D products are summed in fp32 (2^-24 each): an error ds of
     a score changes a weight by about ds, numerator and denominator each.
@@ -264,7 +266,7 @@ def attention_bound(a, parent, q, scale):
                 A = vs.max(0)[None, :]                       # at least sum p |v| / sum p
                 bound[b, :n, h] = (2.0 ** -8 * np.abs(np.nan_to_num(ref[b, :n, h]))
                                    + A * (2.0 ** -9 + 2.0 ** -11 + 2.5 * ds[:, None])
-                                   + 2.0 ** -11 * vs.max(initial=0.0))
+                                   + 2.0 ** -9.8 * vs.max(initial=0.0))
     return ref, bound
 
 
