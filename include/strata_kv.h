@@ -62,7 +62,7 @@ typedef struct {
  *   count    [B] tokens in this call, 0 .. N; NULL = N for every sequence.
  *            Rows of the slots behind a sequence's count are neither read nor
  *            written.
- * B * N < 2^24, max_pages * page < 2^31.  Reported through
+ * B * N < 2^24, B * N * Hkv < 2^29, max_pages * page < 2^31.  Reported through
  * strata_moe_device_status(): a page outside [0, pages) and a position behind
  * max_pages * page (no row is read or written there; attention passes over
  * it), a negative pos and a count outside 0 .. N (the sequence counts as having
@@ -105,7 +105,7 @@ STRATA_API strata_status_t strata_kv_read(strata_kv_cache_t cache, strata_kv_seq
  *            is reported and counts as -1.
  *   q        node i of sequence b at (b * N + i) * q_stride: [Hq][D] bf16
  *   q_stride elements, Hq * D or more, a multiple of 8; 0 = Hq * D
- *   Hq       query heads, Hq % Hkv == 0, Hq / Hkv <= 64
+ *   Hq       query heads, Hq % Hkv == 0, Hq / Hkv <= 64, B * N * Hq < 2^30
  *   scale    <= 0 means 1 / sqrt(D)
  *   out      [B][N][Hq][D] bf16; rows of slots behind count[b] are left as they
  *            were; a node that sees no row gets zeros

@@ -57,7 +57,7 @@ strata_status_t check_tree_dims(const strata_kv_cache_t& c, const strata_kv_seqs
   if (st == STRATA_OK) st = check_seqs_dims(c, s);
   if (st != STRATA_OK) return st;
   if (Hq <= 0 || Hq % c.Hkv) return STRATA_ERR_INVALID_ARG;
-  if (s.N > STRATA_TREE_MAX_NODES || Hq / c.Hkv > 64 || Hq > 65535 || s.B > 65535)
+  if (s.N > STRATA_TREE_MAX_NODES || Hq / c.Hkv > 64 || (int64_t)s.B * s.N * Hq >= (1 << 30))
     return STRATA_ERR_UNSUPPORTED;
   return STRATA_OK;
 }

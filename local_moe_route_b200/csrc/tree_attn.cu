@@ -48,58 +48,83 @@
 
 namespace strata {
 
+#ifndef TA_C16
+#define TA_C16 16
+#endif
+#ifndef TA_OV
+#define TA_OV 2
+#endif
 namespace ta {
-constexpr int TILE = 128;                   // positions per tile
+constexpr int SUB = 128;                    // positions per MMA tile
+constexpr int TILE = 2 * SUB;               // positions per softmax step
 constexpr int NODES = STRATA_TREE_MAX_NODES;
 constexpr int MAX_CTAS = 148 * 4;           // runs the workspace has room for
 constexpr float WSCALE = 448.f;             // weights are scaled to e4m3's largest value
+// What a unit costs besides its tiles (its query rows, the tree's masks, its
+// results), in tiles: units take that much more of the line.
+constexpr int UNIT_COST = TA_OV;
+constexpr int UNITS = 4;                    // units announced ahead
 
 template <int D, int R>
 struct Cfg {
-  static constexpr int NWG = R == 64 ? 2 : 1;          // softmax warpgroups
-  static constexpr int C = R / NWG;                    // row columns per warpgroup
+  static constexpr int C = R == 16 ? TA_C16 : 16;      // row columns per softmax warpgroup
+  static constexpr int NWG = R / C;
   static constexpr int CTAS = R == 64 ? 1 : 2;         // per SM
-  static constexpr int STAGES =
-      D == 128 ? (R == 64 ? 5 : R == 32 ? 2 : 3) : (R == 64 ? 8 : R == 32 ? 5 : 6);
-  static constexpr int THREADS = NWG * 128 + 64;
-  static constexpr int KV_BYTES = TILE * D;            // one operand tile
+  static constexpr int NS = R == 16 ? 2 : 1;           // score tiles in TMEM
+  // K and V rings, in MMA tiles
+  static constexpr int KS = (R == 64 ? 4 : R == 32 ? 2 : 4) * (D == 64 ? 2 : 1);
+  static constexpr int VS = (R == 64 ? 4 : 2) * (D == 64 ? 2 : 1);
+  static constexpr int ES = KS / 2 + NS + 1;           // exponents, in softmax tiles
+  static constexpr int SOFT = NWG * 128;
+  static constexpr int THREADS = SOFT + 64;
+  static constexpr int KV_BYTES = SUB * D;             // one operand tile
   static constexpr int K_OFF = 0;
-  static constexpr int V_OFF = K_OFF + STAGES * KV_BYTES;
-  static constexpr int Q_OFF = V_OFF + STAGES * KV_BYTES;      // [2R][D] codes
-  static constexpr int P_OFF = Q_OFF + 2 * R * D;              // [128][2R] codes
-  static constexpr int E_OFF = P_OFF + TILE * 2 * R;           // [STAGES][2][128] exponents
-  static constexpr int MISC_OFF = E_OFF + STAGES * 256;
-  static constexpr int S_COLS = 2 * R;                 // TMEM: two S tiles, one O tile
-  static constexpr int TMEM_COLS = R == 64 ? 512 : R == 32 ? 256 : 128;
+  static constexpr int V_OFF = K_OFF + KS * KV_BYTES;
+  static constexpr int Q_OFF = V_OFF + VS * KV_BYTES;          // [2R][D] codes
+  static constexpr int P_OFF = Q_OFF + 2 * R * D;              // [TILE][2R] codes
+  static constexpr int E_OFF = P_OFF + TILE * 2 * R;           // [ES][K, V][TILE] exponents
+  static constexpr int MISC_OFF = E_OFF + ES * 2 * TILE;
+  static constexpr int S_COLS = 4 * R;                 // TMEM: NS score tiles, one O tile
+  static constexpr int O_COL = NS * S_COLS;
+  static constexpr int TMEM_COLS = R == 64 ? 512 : 256;
 };
 
-template <int R, int NWG, int C, int STAGES>
+// One unit as a run sees it: tiles first .. stop - 1 of (sequence, KV head,
+// block of rows).
+struct Unit {
+  int b, hk, rb, pos, count, tiles, first, stop, last;
+  unsigned end;              // positions with a column in the page table
+};
+
+template <class F, int R>
 struct Misc {
-  uint64_t full[STAGES], empty[STAGES], s_full[2], p_ready, o_full, q_full;
-  uint64_t sees[R];                  // nodes that the row's node sees
+  uint64_t k_full[F::KS], k_empty[F::KS], v_full[F::VS], v_empty[F::VS], e_full[F::ES];
+  uint64_t s_full[F::NS], p_ready, o_full, q_full, u_full[UNITS], u_empty[UNITS];
+  uint32_t seen_by[NODES][2];        // rows that see the node
   unsigned long long nan_nodes;      // nodes whose V holds a NaN
+  Unit unit[UNITS];
   uint32_t tmem;
   int abort;
   int parent[NODES];
-  int64_t scan[16];
-  int64_t total, start_off;
+  int64_t scan[F::THREADS / 32];
+  int64_t start_off;
   int start_b;
+  int nan_row[R], node[R], head[R];
   alignas(16) float qf[R];                       // score factor of the row
-  int nan_row[R];
-  alignas(16) float wmax[NWG][C][4];             // per warp: largest score of the tile
-  alignas(16) uint32_t wexp[NWG][C][4];          // per warp: largest visible V exponent
-  alignas(16) uint32_t wtop[NWG][4];
-  alignas(16) float mref[NWG][C], beta[NWG][C], alpha[NWG][C];
-  alignas(16) float beta_o[NWG][2][C];
-  alignas(16) uint32_t ecol[NWG][C];
-  alignas(16) float lsum[NWG][C][4];
+  alignas(16) float wmax[F::NWG][4][F::C];       // per warp: largest score of the tile
+  alignas(16) uint32_t wexp[F::NWG][4][F::C];    // per warp: largest visible V exponent
+  uint32_t wtop[F::NWG][4];
+  alignas(16) float mref[F::NWG][F::C], beta[F::NWG][F::C], alpha[F::NWG][F::C];
+  alignas(16) float beta_o[F::NWG][2][F::C];
+  alignas(16) float eh[F::NWG][F::C];            // a row's V exponent as a factor
+  alignas(16) float inv[R];                      // 1 / (sum * WSCALE)
 };
 
 // A run's first unit may have begun in an earlier run: slot 0; its last may go
-// on in the next: slot 1.
+// on in the next: slot 1.  Per unit: the run that begins it, and how many
+// runs after that one go on with it.
 struct Head {
-  int follow;      // runs after this one that continue the unit of slot 1
-  int b, hk, rb;
+  int run, follow;
 };
 
 __host__ __device__ constexpr size_t slot_floats(int R, int D) { return (size_t)R * (D + 2); }
@@ -112,6 +137,7 @@ struct TreeArgs {
   const uint16_t* q;
   int64_t q_stride;
   int Hq, G;              // query heads, query heads per KV head
+  int blocks;             // blocks of R rows per sequence and KV head when it has N nodes
   float scale;            // times log2(e)
   uint16_t* out;
   ta::Head* heads;
@@ -122,7 +148,10 @@ struct TreeArgs {
 // One sequence's extent in this call.
 struct TreeSeq {
   int pos, count, tiles, blocks;
-  int64_t end;            // positions with a column in the page table
+  unsigned end;           // positions with a column in the page table
+  __device__ __forceinline__ int64_t length(const TreeArgs& a) const {   // in the line
+    return tiles ? (int64_t)(tiles + ta::UNIT_COST) * blocks * a.c.Hkv : 0;
+  }
 };
 
 template <int R>
@@ -132,8 +161,8 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool repor
   const SeqRange r = seq_range(a.s, b, &bad);
   t.pos = r.pos;
   t.count = r.count;
-  const int64_t room = (int64_t)a.s.max_pages * a.c.page;
-  t.end = (int64_t)r.pos + r.count;
+  const unsigned room = (unsigned)a.s.max_pages * (unsigned)a.c.page;
+  t.end = (unsigned)r.pos + (unsigned)r.count;
   if (t.end > room) {
     bad = r.count > 0;
     t.end = room;
@@ -144,22 +173,26 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool repor
   return t;
 }
 
-// A run's position in the line of tiles.
+// The units of a run in order.  A unit takes UNIT_COST + tiles places of the
+// line; a run that holds only its first places leaves all its tiles to
+// the next run.
 template <int R>
 struct Cursor {
-  int b, hk, rb, tile;
   TreeSeq t;
-  __device__ __forceinline__ void at(const TreeArgs& a, int b0, int64_t off) {
+  int b, hk, rb;
+  int64_t off;            // place in the unit
+  int64_t left;           // places left in the run
+  __device__ __forceinline__ void start(const TreeArgs& a, int b0, int64_t o, int64_t n) {
     b = b0;
+    left = n;
     t = tree_seq<R>(a, b, false);
-    tile = (int)(off % t.tiles);
-    const int64_t u = off / t.tiles;
+    const int64_t len = t.tiles + ta::UNIT_COST, u = o / len;
+    off = o % len;
     rb = (int)(u % t.blocks);
     hk = (int)(u / t.blocks);
   }
-  // To the next unit; only called while tiles are left in the run.
-  __device__ __forceinline__ void next_unit(const TreeArgs& a) {
-    tile = 0;
+  __device__ __forceinline__ void advance(const TreeArgs& a) {
+    off = 0;
     if (++rb < t.blocks) return;
     rb = 0;
     if (++hk < a.c.Hkv) return;
@@ -169,7 +202,42 @@ struct Cursor {
       t = tree_seq<R>(a, b, false);
     } while (t.tiles == 0);
   }
+  // The next unit with tiles in this run; false when there is none.
+  __device__ __forceinline__ bool next(const TreeArgs& a, ta::Unit* u) {
+    while (left > 0) {
+      const int64_t len = t.tiles + ta::UNIT_COST;
+      const int64_t upto = min(len, off + left);
+      const int first = (int)max((int64_t)0, off - ta::UNIT_COST);
+      const int stop = (int)max((int64_t)0, upto - ta::UNIT_COST);
+      const ta::Unit x = {b, hk, rb, t.pos, t.count, t.tiles, first, stop, 0, t.end};
+      left -= upto - off;
+      if (left > 0) advance(a);
+      if (stop > first) {
+        *u = x;
+        return true;
+      }
+    }
+    return false;
+  }
 };
+
+// 32 lanes x N consecutive columns, waited for.
+template <int N>
+__device__ __forceinline__ void tmem_load2(uint32_t at0, uint32_t at1, uint32_t (&x)[N],
+                                           uint32_t (&y)[N]) {
+  if constexpr (N == 16) {
+    tmem_ld_32x32b_x16(at0, x);
+    tmem_ld_32x32b_x16(at1, y);
+    tmem_ld_wait_regs(x);
+    tmem_ld_wait_regs(y);
+  } else {
+    static_assert(N == 8, "columns per warpgroup");
+    tmem_ld_32x32b_x8(at0, x);
+    tmem_ld_32x32b_x8(at1, y);
+    tmem_ld_wait_regs(x);
+    tmem_ld_wait_regs(y);
+  }
+}
 
 __device__ __forceinline__ float ta_exp2(float x) {
   float y;
@@ -245,14 +313,26 @@ __device__ __forceinline__ void split4(uint32_t h01, uint32_t h23, uint32_t* hi,
   }
 }
 
+// Waits (with a limit) for the copies in flight into a ring of N stages, of
+// which `n` uses were armed: shared memory must outlive them.
+template <int N>
+__device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t n) {
+  for (uint32_t i = n > (uint32_t)N ? n - N : 0; i < n; ++i) {
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait(smem_addr(&full[i % N]), (i / N) & 1) &&
+           global_ns() - t0 < kWaitLimitNs) {
+    }
+  }
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     tree_attn_kernel(const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const TreeArgs a) {
   using namespace ta;
   using F = Cfg<D, R>;
-  constexpr int NWG = F::NWG, C = F::C, STAGES = F::STAGES;
-  using M = Misc<R, NWG, C, STAGES>;
+  constexpr int NWG = F::NWG, C = F::C, KS = F::KS, VS = F::VS, ES = F::ES, NS = F::NS;
+  using M = Misc<F, R>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sK = smem + F::K_OFF;
   uint8_t* sV = smem + F::V_OFF;
@@ -267,17 +347,24 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (th == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&m.full[i], 1);
-      mbar_init(&m.empty[i], 1);
+    for (int i = 0; i < KS; ++i) {
+      mbar_init(&m.k_full[i], 1);
+      mbar_init(&m.k_empty[i], 1);
     }
-    mbar_init(&m.s_full[0], 1);
-    mbar_init(&m.s_full[1], 1);
-    mbar_init(&m.p_ready, NWG * 128);
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(&m.v_full[i], 1);
+      mbar_init(&m.v_empty[i], 1);
+    }
+    for (int i = 0; i < ES; ++i) mbar_init(&m.e_full[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&m.s_full[i], 1);
+    mbar_init(&m.p_ready, F::SOFT);
     mbar_init(&m.o_full, 1);
-    mbar_init(&m.q_full, NWG * 128);
+    mbar_init(&m.q_full, F::SOFT);
+    for (int i = 0; i < UNITS; ++i) {
+      mbar_init(&m.u_full[i], 1);
+      mbar_init(&m.u_empty[i], 2);       // the MMA warp and the softmax
+    }
     m.abort = 0;
-    m.start_b = -1;
     fence_mbar_init();
   }
   if (warp == W_TMA && lane == 0) {
@@ -286,15 +373,12 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
   }
   if (warp == W_MMA) tmem_alloc(&m.tmem, F::TMEM_COLS);
 
-  // ---- the line of tiles and this CTA's run of it: sequences in contiguous
-  // shares per thread, their tile counts scanned over the CTA
+  // ---- the line and this CTA's run of it: sequences in contiguous shares per
+  // thread, their lengths scanned over the CTA
   const int per = (a.s.B + F::THREADS - 1) / F::THREADS;
   const int sb0 = min(th * per, a.s.B), sb1 = min(sb0 + per, a.s.B);
   int64_t mine = 0;
-  for (int b = sb0; b < sb1; ++b) {
-    const TreeSeq t = tree_seq<R>(a, b, reporter);
-    mine += (int64_t)t.tiles * t.blocks * a.c.Hkv;
-  }
+  for (int b = sb0; b < sb1; ++b) mine += tree_seq<R>(a, b, reporter).length(a);
   int64_t incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -310,7 +394,9 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     if (w < warp) before += m.scan[w];
     total += m.scan[w];
   }
-  const int64_t runs = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
+  // no run shorter than a unit's cost and a tile
+  const int64_t most = (total + UNIT_COST) / (UNIT_COST + 1);
+  const int64_t runs = most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x;
   const int cta = blockIdx.x;
   const bool active = cta < runs;
   const int64_t w0 = active ? total * cta / runs : 0;
@@ -318,8 +404,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
   if (active && w0 >= before && w0 < before + mine) {
     int64_t at = before;
     for (int b = sb0; b < sb1; ++b) {
-      const TreeSeq t = tree_seq<R>(a, b, false);
-      const int64_t n = (int64_t)t.tiles * t.blocks * a.c.Hkv;
+      const int64_t n = tree_seq<R>(a, b, false).length(a);
       if (w0 < at + n) {
         m.start_b = b;
         m.start_off = w0 - at;
@@ -329,130 +414,219 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     }
   }
   __syncthreads();
-  const int64_t n_items = w1 - w0;
   const uint32_t tmem = m.tmem;
   if (!active) {
-    if (th == 0) a.heads[cta].follow = 0;
+    // more runs than work
   } else if (warp == W_TMA) {
-    // ------------------------------------------------------------ page copies
+    // ------------------------------------------------ units and page copies
+    // In the order in which the places come free: exponents and K of a tile,
+    // then V of the tile before it.
     Cursor<R> cu;
-    cu.at(a, m.start_b, m.start_off);
-    const int page = a.c.page, ppt = TILE / page;      // pages per tile
-    uint32_t g = 0;
-    int64_t left = n_items;
-    while (left > 0) {
-      const int stop = (int)min((int64_t)cu.t.tiles, (int64_t)cu.tile + left);
-      left -= stop - cu.tile;
-      bool dead = false;
-      for (; cu.tile < stop; ++cu.tile, ++g) {
-        const int st = g % STAGES;
-        // the tile's pages, one per lane
-        const int64_t first = (int64_t)cu.tile * TILE + (int64_t)lane * page;
-        int64_t row = -1;
-        if (lane < ppt && first < cu.t.end) {
-          row = row_of(a.c, a.s, cu.b, first);
-          if (row < 0)
-            atomicOr(a.err, kErrIndex);
-          else
-            row += (int64_t)cu.hk * page;
+    cu.start(a, m.start_b, m.start_off, w1 - w0);
+    uint32_t jk = 0, jv = 0, g = 0, un = 0;
+    int64_t row[2] = {-1, -1};         // of the tile, per MMA tile: this lane's page
+    bool dead = false;
+    const int page = a.c.page;
+    auto load_k = [&]() -> bool {
+#pragma unroll
+      for (int h = 0; h < 2; ++h, ++jk) {
+        const int ks = jk % KS;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, row[h] >= 0));
+        if (jk >= (uint32_t)KS &&
+            !mbar_wait_warp(&m.k_empty[ks], (jk / KS - 1) & 1, abort_flag, a.err))
+          return false;
+        if (lane == 0) mbar_arrive_expect_tx(&m.k_full[ks], n * page * D);
+        __syncwarp();
+        if (row[h] >= 0)
+          tma_load_2d(sK + ks * F::KV_BYTES + lane * page * D, &map_k, 0, (int)row[h],
+                      &m.k_full[ks]);
+      }
+      return true;
+    };
+    auto load_v = [&]() -> bool {
+#pragma unroll
+      for (int h = 0; h < 2; ++h, ++jv) {
+        const int vs = jv % VS;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, row[h] >= 0));
+        if (jv >= (uint32_t)VS &&
+            !mbar_wait_warp(&m.v_empty[vs], (jv / VS - 1) & 1, abort_flag, a.err))
+          return false;
+        if (lane == 0) mbar_arrive_expect_tx(&m.v_full[vs], n * page * D);
+        __syncwarp();
+        if (row[h] >= 0)
+          tma_load_2d(sV + vs * F::KV_BYTES + lane * page * D, &map_v, 0, (int)row[h],
+                      &m.v_full[vs]);
+      }
+      return true;
+    };
+    // The slot's last tile is done with: this warp has waited for the K tile
+    // KS / 2 tiles back, whose scores were taken after the weights NS + KS / 2
+    // tiles back were finished.
+    auto load_e = [&]() {
+      const int es = g % ES;
+      uint8_t* e = sE + es * 2 * TILE + lane * page;
+      uint32_t n = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        n += __popc(__ballot_sync(0xffffffffu, row[h] >= 0));
+        if (lane * page < SUB && row[h] < 0) {         // no page: nothing held there
+          for (int i = 0; i < page; i += 16)
+            *reinterpret_cast<uint4*>(e + h * SUB + i) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();                    // before a later copy to the same place
         }
-        if (g >= (uint32_t)STAGES &&
-            !mbar_wait_warp(&m.empty[st], (g / STAGES - 1) & 1, abort_flag, a.err)) {
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&m.e_full[es], n * page * 2);
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (row[h] >= 0) {
+          bulk_load(e + h * SUB, a.c.k_exp + row[h], page, &m.e_full[es]);
+          bulk_load(e + TILE + h * SUB, a.c.v_exp + row[h], page, &m.e_full[es]);
+        }
+      ++g;
+    };
+    while (!dead) {
+      Unit u;
+      const bool some = cu.next(a, &u);
+      const int us = un % UNITS;
+      if (un >= (uint32_t)UNITS &&
+          !mbar_wait_warp(&m.u_empty[us], (un / UNITS - 1) & 1, abort_flag, a.err)) {
+        dead = true;
+        break;
+      }
+      if (lane == 0) {
+        if (some) m.unit[us] = u;
+        m.unit[us].last = !some;       // an entry without tiles ends the run
+        mbar_arrive(&m.u_full[us]);
+      }
+      __syncwarp();
+      ++un;
+      if (!some) break;
+      for (int tile = u.first; tile < u.stop; ++tile) {
+        int64_t now[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const unsigned t = (unsigned)tile * TILE + h * SUB + (unsigned)(lane * page);
+          now[h] = -1;
+          if (lane * page < SUB && t < u.end) {
+            now[h] = row_of(a.c, a.s, u.b, t);
+            if (now[h] < 0)
+              atomicOr(a.err, kErrIndex);
+            else
+              now[h] += (int64_t)u.hk * page;
+          }
+        }
+        const int64_t was[2] = {row[0], row[1]};
+        row[0] = now[0];
+        row[1] = now[1];
+        // the exponents' slot is free once the first K place is
+        if (jk >= (uint32_t)KS &&
+            !mbar_wait_warp(&m.k_empty[jk % KS], (jk / KS - 1) & 1, abort_flag, a.err)) {
           dead = true;
           break;
         }
-        uint8_t* e = sE + st * 256;
-        if (lane < ppt && row < 0) {                   // no page: nothing held there
-          for (int i = 0; i < page; i += 16)
-            *reinterpret_cast<uint4*>(e + lane * page + i) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();                    // before a later copy to the same place
+        load_e();
+        if (!load_k()) {
+          dead = true;
+          break;
         }
-        const uint32_t pages = __popc(__ballot_sync(0xffffffffu, row >= 0));
-        if (lane == 0) mbar_arrive_expect_tx(&m.full[st], pages * page * (2 * D + 2));
-        __syncwarp();
-        if (row >= 0) {
-          tma_load_2d(sK + st * F::KV_BYTES + lane * page * D, &map_k, 0, (int)row, &m.full[st]);
-          tma_load_2d(sV + st * F::KV_BYTES + lane * page * D, &map_v, 0, (int)row, &m.full[st]);
-          bulk_load(e + lane * page, a.c.k_exp + row, page, &m.full[st]);
-          bulk_load(e + 128 + lane * page, a.c.v_exp + row, page, &m.full[st]);
-        }
-        __syncwarp();
-      }
-      if (dead) {
-        // copies in flight land before the CTA's shared memory goes away
-        for (uint32_t i = g > (uint32_t)STAGES ? g - STAGES : 0; i < g; ++i) {
-          const uint32_t bar = smem_addr(&m.full[i % STAGES]);
-          const unsigned long long t0 = global_ns();
-          while (!mbar_try_wait(bar, (i / STAGES) & 1) && global_ns() - t0 < kWaitLimitNs) {
+        if (g > 1) {
+          row[0] = was[0];
+          row[1] = was[1];
+          if (!load_v()) {
+            dead = true;
+            break;
           }
+          row[0] = now[0];
+          row[1] = now[1];
         }
-        break;
       }
-      if (left > 0) cu.next_unit(a);
+    }
+    if (!dead && g > 0) dead = !load_v();
+    if (dead) {
+      drain_ring<KS>(m.k_full, jk);
+      drain_ring<VS>(m.v_full, jv);
+      drain_ring<ES>(m.e_full, g);
     }
   } else if (warp == W_MMA) {
-    // ------------------------------------------------------------ MMA issue
+    // ------------------------------------------------ MMA issue
     const bool leader = elect_one();
-    constexpr uint32_t ID_S = idesc_e4m3(TILE, 2 * R, 0, 0);
+    constexpr uint32_t ID_S = idesc_e4m3(SUB, 2 * R, 0, 0);
     constexpr uint32_t ID_O = idesc_e4m3(D, 2 * R, 1, 1);
-    const uint32_t t_o = tmem + 2 * F::S_COLS;
-    uint32_t g = 0, unit = 0;
+    uint32_t g = 0;                                        // tiles
     auto scores = [&](uint32_t i) -> bool {
-      const int st = i % STAGES;
-      if (!mbar_wait_warp(&m.full[st], (i / STAGES) & 1, abort_flag, a.err)) return false;
-      tc_fence_after();
-      if (leader) {
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t j = 2 * i + h;
+        const int ks = j % KS;
+        if (!mbar_wait_warp(&m.k_full[ks], (j / KS) & 1, abort_flag, a.err)) return false;
+        tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          mma_f8_ss(tmem + (i & 1) * F::S_COLS,
-                    smem_desc(smem_addr(sK + st * F::KV_BYTES) + 32 * k, 8 * D, sw_mode(D)),
-                    smem_desc(smem_addr(sQ) + 32 * k, 8 * D, sw_mode(D)), ID_S, k > 0);
-        mma_commit(&m.s_full[i & 1]);
+          for (int k = 0; k < D / 32; ++k)
+            mma_f8_ss(tmem + (i % NS) * F::S_COLS + h * 2 * R,
+                      smem_desc(smem_addr(sK + ks * F::KV_BYTES) + 32 * k, 8 * D, sw_mode(D)),
+                      smem_desc(smem_addr(sQ) + 32 * k, 8 * D, sw_mode(D)), ID_S, k > 0);
+          mma_commit(&m.k_empty[ks]);
+          if (h == 1) mma_commit(&m.s_full[i % NS]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       return true;
     };
-    Cursor<R> cu;
-    cu.at(a, m.start_b, m.start_off);
-    int64_t left = n_items;
+    auto output = [&](uint32_t i) -> bool {
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t j = 2 * i + h;
+        const int vs = j % VS;
+        if (!mbar_wait_warp(&m.v_full[vs], (j / VS) & 1, abort_flag, a.err)) return false;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < SUB / 32; ++k)
+            mma_f8_ss(tmem + F::O_COL,
+                      smem_desc(smem_addr(sV + vs * F::KV_BYTES) + 32 * k * D, 8 * D, sw_mode(D)),
+                      smem_desc(smem_addr(sP) + (h * SUB + 32 * k) * 2 * R, 16 * R,
+                                sw_mode(2 * R)),
+                      ID_O, h > 0 || k > 0);
+          mma_commit(&m.v_empty[vs]);
+          if (h == 1) mma_commit(&m.o_full);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
     bool dead = false;
-    while (left > 0 && !dead) {
-      const int tiles = (int)min((int64_t)cu.t.tiles - cu.tile, left);
-      left -= tiles;
-      if (!mbar_wait_warp(&m.q_full, unit & 1, abort_flag, a.err)) break;
+    for (uint32_t un = 0; !dead; ++un) {
+      const int us = un % UNITS;
+      if (!mbar_wait_warp(&m.u_full[us], (un / UNITS) & 1, abort_flag, a.err)) break;
+      const int tiles = m.unit[us].stop - m.unit[us].first;
+      const bool last = m.unit[us].last;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.u_empty[us]);
+      if (last) break;
+      if (!mbar_wait_warp(&m.q_full, un & 1, abort_flag, a.err)) break;
       tc_fence_after();
       if (!scores(g)) break;
       for (int i = 0; i < tiles; ++i, ++g) {
-        const int st = g % STAGES;
-        if (i + 1 < tiles && !scores(g + 1)) {
-          dead = true;
-          break;
-        }
-        if (!mbar_wait_warp(&m.p_ready, g & 1, abort_flag, a.err)) {
+        const bool more = i + 1 < tiles;
+        // the next scores as early as their place in TMEM allows
+        if (NS == 2 && more && !scores(g + 1)) dead = true;
+        if (dead || !mbar_wait_warp(&m.p_ready, g & 1, abort_flag, a.err)) {
           dead = true;
           break;
         }
         tc_fence_after();
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < TILE / 32; ++k)
-            mma_f8_ss(t_o,
-                      smem_desc(smem_addr(sV + st * F::KV_BYTES) + 32 * k * D, 8 * D, sw_mode(D)),
-                      smem_desc(smem_addr(sP) + 32 * k * 2 * R, 16 * R, sw_mode(2 * R)), ID_O,
-                      k > 0);
-          mma_commit(&m.o_full);
-          mma_commit(&m.empty[st]);
+        if ((NS == 1 && more && !scores(g + 1)) || !output(g)) {
+          dead = true;
+          break;
         }
-        __syncwarp();
       }
-      ++unit;
-      if (left > 0 && !dead) cu.next_unit(a);
     }
   } else {
-    // ------------------------------------------------------------ softmax
-    const int wg = warp / 4, wq = warp % 4, lt = th % 128;   // lt: position in the tile
-    constexpr uint32_t ALL = NWG * 128;
-    const uint32_t lanes_at = tmem + ((uint32_t)(wq * 32) << 16);
+    // ------------------------------------------------ softmax
+    const int wg = warp / 4, wq = warp % 4, lt = th % 128;   // lt: position in an MMA tile
+    constexpr uint32_t ALL = F::SOFT;
+    const uint32_t lanes_at = tmem + ((uint32_t)(wq * 32) << 16) + wg * C;
     const uint32_t bar_wg = 2 + wg;
     // the feature whose sums this thread keeps (D = 64: 16 lanes per warp)
     const int feat = D == 128 ? lt : wq * 16 + lane;
@@ -460,116 +634,102 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     float acc[C], l[C];
     uint32_t g = 0;
     bool ok = true, dead = false;
-    int64_t left = n_items;
-    Cursor<R> cu;
-    cu.at(a, m.start_b, m.start_off);
-    if (th == 0) a.heads[cta].follow = 0;
 
     // O of tile i (sum of its high and low columns) into acc
     auto add_o = [&](uint32_t i) {
       ok = mbar_wait_warp(&m.o_full, i & 1, abort_flag, a.err) && ok;
       tc_fence_after();
       const float* bo = m.beta_o[wg][i & 1];
+      uint32_t hi[C], lo[C];
+      tmem_load2<C>(lanes_at + F::O_COL, lanes_at + F::O_COL + R, hi, lo);
 #pragma unroll
-      for (int c0 = 0; c0 < C; c0 += 16) {
-        uint32_t hi[16], lo[16];
-        const uint32_t col = lanes_at + 2 * F::S_COLS + wg * C + c0;
-        tmem_ld_32x32b_x16(col, hi);
-        tmem_ld_32x32b_x16(col + R, lo);
-        tmem_ld_wait_regs(hi);
-        tmem_ld_wait_regs(lo);
+      for (int c = 0; c < C; c += 4) {
+        const float4 b4 = *reinterpret_cast<const float4*>(bo + c);
+        const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-          const float4 b4 = *reinterpret_cast<const float4*>(bo + c0 + c);
-          const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[c0 + c + j] = fmaf(__uint_as_float(hi[c + j]) + __uint_as_float(lo[c + j]), bb[j],
-                                   acc[c0 + c + j]);
-        }
+        for (int j = 0; j < 4; ++j)
+          acc[c + j] =
+              fmaf(__uint_as_float(hi[c + j]) + __uint_as_float(lo[c + j]), bb[j], acc[c + j]);
       }
     };
 
     // The unit's results: rounded to the output when the run holds all of it,
     // its part otherwise.
-    auto finish_unit = [&](int first_tile, int stop, bool drafts) {
-      unsigned long long nan_nodes = drafts ? m.nan_nodes : 0;
+    auto finish_unit = [&](const Unit& u) {
+      unsigned long long nan_nodes = (unsigned)u.stop * TILE > (unsigned)u.pos ? m.nan_nodes : 0;
       while (nan_nodes) {
         const int j = __ffsll((long long)nan_nodes) - 1;
         nan_nodes &= nan_nodes - 1;
-        const int64_t row = row_of(a.c, a.s, cu.b, (int64_t)cu.t.pos + j) + (int64_t)cu.hk * a.c.page;
-        if (has_feat && (a.c.v[row * D + feat] & 0x7F) == 0x7F) {
+        const int64_t row = row_of(a.c, a.s, u.b, (int64_t)u.pos + j) + (int64_t)u.hk * a.c.page;
+        const bool nan = has_feat && (a.c.v[row * D + feat] & 0x7F) == 0x7F;
+        const uint32_t by = m.seen_by[j][wg * C / 32] >> (wg * C % 32);
 #pragma unroll
-          for (int c = 0; c < C; ++c)
-            if ((m.sees[wg * C + c] >> j) & 1) acc[c] = __uint_as_float(0x7FC00000u);
-        }
+        for (int c = 0; c < C; ++c)
+          if (nan && ((by >> c) & 1)) acc[c] = __uint_as_float(0x7FC00000u);
       }
-      const bool whole = first_tile == 0 && stop == cu.t.tiles;
-      const int slot = first_tile == 0 ? 1 : 0;
-      float* part = a.parts + (size_t)(2 * cta + slot) * slot_floats(R, D);
-      if (!whole && slot == 1 && th == 0) {
+      const bool whole = u.first == 0 && u.stop == u.tiles;
+      if (u.first == 0 && th == 0) {
         // the last run that holds a tile of this unit: the unit ends
         // (tiles - stop) tiles behind this run
-        const int64_t last = w1 + (cu.t.tiles - stop) - 1;
         Head hd;
-        hd.follow = (int)(((last + 1) * runs - 1) / total) - cta;
-        hd.b = cu.b;
-        hd.hk = cu.hk;
-        hd.rb = cu.rb;
-        a.heads[cta] = hd;
+        hd.run = cta;
+        hd.follow = whole ? 0 : (int)(((w1 + (u.tiles - u.stop)) * runs - 1) / total) - cta;
+        a.heads[((int64_t)u.b * a.c.Hkv + u.hk) * a.blocks + u.rb] = hd;
       }
+      if (!has_feat) return;
+      if (whole) {
+        uint16_t* out = a.out + (int64_t)u.b * a.s.N * a.Hq * D + feat;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int r = wg * C + c;
-        const float4 l4 = *reinterpret_cast<const float4*>(m.lsum[wg][c]);
-        float sum = (l4.x + l4.y) + (l4.z + l4.w);
-        if (m.nan_row[r]) sum = __uint_as_float(0x7FC00000u);
-        if (whole) {
-          const int flat = cu.rb * R + r;
-          const int node = flat / a.G, h = cu.hk * a.G + flat % a.G;
-          if (node < cu.t.count && has_feat) {
-            const float o = sum == 0.f ? 0.f : acc[c] / (sum * WSCALE);
-            a.out[(((int64_t)cu.b * a.s.N + node) * a.Hq + h) * D + feat] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(o));
-          }
-        } else {
-          if (has_feat) part[r * D + feat] = acc[c];
-          if (lt == 0) {
-            part[R * D + 2 * r] = m.mref[wg][c];
-            part[R * D + 2 * r + 1] = sum;
-          }
+        for (int c = 0; c < C; ++c) {
+          const int r = wg * C + c;
+          if (m.node[r] < u.count)
+            out[(int64_t)(m.node[r] * a.Hq + m.head[r]) * D] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(acc[c] * m.inv[r]));
         }
+      } else {
+        float* part = a.parts + (size_t)(2 * cta + (u.first == 0)) * slot_floats(R, D) +
+                      wg * C * D + feat;
+#pragma unroll
+        for (int c = 0; c < C; ++c) part[c * D] = acc[c];
       }
     };
 
-    for (;;) {
+    for (uint32_t un = 0;; ++un) {
       // ---- a unit begins: its query rows, split and scaled, and what they see
-      const int first_tile = cu.tile;
-      const int stop = (int)min((int64_t)cu.t.tiles, (int64_t)cu.tile + left);
-      left -= stop - first_tile;
-      const int pos = cu.t.pos;
-      const bool drafts = (int64_t)stop * TILE > pos;        // the run reaches the tree
+      const Unit& u = m.unit[un % UNITS];
+      dead = !mbar_wait_warp(&m.u_full[un % UNITS], (un / UNITS) & 1, abort_flag, a.err);
+      if (named_barrier_or(1, ALL, dead)) break;
+      if (u.last) break;
+      const unsigned pos = (unsigned)u.pos;
+      const bool drafts = (unsigned)u.stop * TILE > pos;     // the run reaches the tree
+      if (th < R) {
+        const int flat = u.rb * R + th;
+        m.node[th] = flat / a.G;
+        m.head[th] = u.hk * a.G + flat % a.G;
+      }
       if (th < NODES && drafts) {
         int p = -1;
-        if (th < cu.t.count) {
-          p = a.parent ? a.parent[(int64_t)cu.b * a.s.N + th] : th - 1;
+        if (th < u.count) {
+          p = a.parent ? a.parent[(int64_t)u.b * a.s.N + th] : th - 1;
           if (p < -1 || p >= th) {
             atomicOr(a.err, kErrIndex);
             p = -1;
           }
         }
         m.parent[th] = p;
+        m.seen_by[th][0] = m.seen_by[th][1] = 0;
       }
       if (th == 0) m.nan_nodes = 0;
+      named_barrier_sync(1, ALL);
       constexpr int LPR = D / 8;             // lanes per row, 8 values each
+#pragma unroll 1
       for (int r0 = 0; r0 < R; r0 += ALL / LPR) {
         const int r = r0 + th / LPR, ch = th % LPR;
         if (r0 + ALL / LPR > R && r >= R) continue;
-        const int flat = cu.rb * R + r;
-        const int node = flat / a.G, h = cu.hk * a.G + flat % a.G;
+        const int node = m.node[r];
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (node < cu.t.count)
-          x = ld_nc_v4(a.q + ((int64_t)cu.b * a.s.N + node) * a.q_stride + (int64_t)h * D + ch * 8);
+        if (node < u.count)
+          x = ld_nc_v4(a.q + ((int64_t)u.b * a.s.N + node) * a.q_stride + m.head[r] * D + ch * 8);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
         uint32_t top = 0;
 #pragma unroll
@@ -580,19 +740,18 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         const bool nan = top >= 0x7F80u;     // an infinity's scores are NaN as well
         int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
         e = nan ? 0 : min(max(e, -126), 119);
-        const float s = nan ? 0.f : pow2i(-e);
+        const float s = pow2i(-e);
         uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-        if (!nan) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 y = make_float2(bf16_lo(w[i]) * s, bf16_hi(w[i]) * s);
-            const __nv_fp8x2_storage_t c8 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-            const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c8, __NV_E4M3)));
-            const __nv_fp8x2_storage_t r8 = __nv_cvt_float2_to_fp8x2(
-                make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
-            hi[i / 2] |= (uint32_t)c8 << (16 * (i & 1));
-            lo[i / 2] |= (uint32_t)r8 << (16 * (i & 1));
-          }
+        for (int i = 0; i < 4; ++i) {
+          if (nan) break;
+          const float2 y = make_float2(bf16_lo(w[i]) * s, bf16_hi(w[i]) * s);
+          const __nv_fp8x2_storage_t c8 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+          const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c8, __NV_E4M3)));
+          const __nv_fp8x2_storage_t r8 = __nv_cvt_float2_to_fp8x2(
+              make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
+          hi[i / 2] |= (uint32_t)c8 << (16 * (i & 1));
+          lo[i / 2] |= (uint32_t)r8 << (16 * (i & 1));
         }
         *reinterpret_cast<uint2*>(sQ + sw_off<D>(r, ch * 8)) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2*>(sQ + sw_off<D>(R + r, ch * 8)) = make_uint2(lo[0], lo[1]);
@@ -602,100 +761,88 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         }
       }
       fence_proxy_async_smem();
-      named_barrier_sync(1, ALL);
-      if (drafts && th < R) {
-        const int node = min((cu.rb * R + th) / a.G, NODES - 1);
-        uint64_t see = 0;
-        for (int j = node; j >= 0; j = m.parent[j]) see |= 1ull << j;
-        m.sees[th] = see;
-      }
-      named_barrier_sync(1, ALL);
       mbar_arrive(&m.q_full);
+      if (drafts && th < R)
+        for (int j = min(m.node[th], NODES - 1); j >= 0; j = m.parent[j])
+          atomicOr(&m.seen_by[j][th / 32], 1u << (th % 32));
+      named_barrier_sync(1, ALL);
 
       float m_run = -INFINITY;               // of column lt, in threads lt < C
 #pragma unroll
       for (int c = 0; c < C; ++c) acc[c] = l[c] = 0.f;
+      const int first_tile = u.first, stop = u.stop;
+      const unsigned end = u.end;
       for (int tile = first_tile; tile < stop; ++tile, ++g) {
-        const int st = g % STAGES;
-        ok = mbar_wait_warp(&m.full[st], (g / STAGES) & 1, abort_flag, a.err) && ok;
-        const int64_t t = (int64_t)tile * TILE + lt;
-        const uint32_t ke = sE[st * 256 + lt], ve = sE[st * 256 + 128 + lt];
-        const bool held = t < cu.t.end && ke != 0;
-        const bool tree = (int64_t)(tile + 1) * TILE > pos;  // some positions are nodes
-        const int node = t >= pos ? (int)(t - pos) : -1;     // >= 0: this one is
-        const float kf = __uint_as_float(ke << 23);
-        if (wg == 0) {
-          // V rows that must not reach the product: nothing held (stale
-          // bytes), or a node's NaN, which only the nodes that see it may get
-          uint4* vr = reinterpret_cast<uint4*>(sV + st * F::KV_BYTES + lt * D);
-          if (!held || ve == 0) {
+        ok = mbar_wait_warp(&m.e_full[g % ES], (g / ES) & 1, abort_flag, a.err) && ok;
+        const uint8_t* e = sE + (g % ES) * 2 * TILE + lt;
+        const uint32_t ke[2] = {e[0], e[SUB]}, ve[2] = {e[TILE], e[TILE + SUB]};
+        const bool tree = (unsigned)(tile + 1) * TILE > pos;  // nodes, or the end
+        // positions to mask or to keep from the product
+        const bool odd =
+            __any_sync(0xffffffffu, tree || !ke[0] || !ke[1] || !ve[0] || !ve[1]);
+        uint32_t vis[2] = {~0u, ~0u};        // rows of this warpgroup that see the position
+        if (odd) {
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) vr[i] = make_uint4(0, 0, 0, 0);
-          } else if (node >= 0) {
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              uint4 x = vr[i];
-              uint32_t n[4] = {__vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
-                               __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
-                               __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
-                               __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)};
-              if (n[0] | n[1] | n[2] | n[3]) {
-                any = true;
-                vr[i] = make_uint4(x.x & ~n[0], x.y & ~n[1], x.z & ~n[2], x.w & ~n[3]);
-              }
-            }
-            if (any) atomicOr(&m.nan_nodes, 1ull << node);
+          for (int h = 0; h < 2; ++h) {
+            const unsigned t = (unsigned)tile * TILE + h * SUB + lt;
+            if (t >= end || ke[h] == 0)
+              vis[h] = 0;
+            else if (t >= pos)
+              vis[h] = m.seen_by[t - pos][wg * C / 32] >> (wg * C % 32);
           }
         }
-        ok = mbar_wait_warp(&m.s_full[g & 1], (g >> 1) & 1, abort_flag, a.err) && ok;
+        ok = mbar_wait_warp(&m.s_full[g % NS], (g / NS) & 1, abort_flag, a.err) && ok;
         tc_fence_after();
-        float s[C];
-        float top_mine = -INFINITY;          // the warp's maximum of column `lane`
-        uint32_t exp_mine = 0;
+        float s[2][C];
 #pragma unroll
-        for (int c0 = 0; c0 < C; c0 += 16) {
-          uint32_t hi[16], lo[16];
-          const uint32_t col = lanes_at + (g & 1) * F::S_COLS + wg * C + c0;
-          tmem_ld_32x32b_x16(col, hi);
-          tmem_ld_32x32b_x16(col + R, lo);
-          tmem_ld_wait_regs(hi);
-          tmem_ld_wait_regs(lo);
+        for (int h = 0; h < 2; ++h) {
+          const float kf = __uint_as_float(ke[h] << 23);
+          uint32_t hi[C], lo[C];
+          const uint32_t col = lanes_at + (g % NS) * F::S_COLS + h * 2 * R;
+          tmem_load2<C>(col, col + R, hi, lo);
 #pragma unroll
-          for (int c = 0; c < 16; c += 4) {
-            const float4 f4 = *reinterpret_cast<const float4*>(&m.qf[wg * C + c0 + c]);
+          for (int c = 0; c < C; c += 4) {
+            const float4 f4 = *reinterpret_cast<const float4*>(&m.qf[wg * C + c]);
             const float ff[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float u = __uint_as_float(hi[c + j]) + __uint_as_float(lo[c + j]);
-              s[c0 + c + j] = held ? u * (ff[j] * kf) : -INFINITY;
-            }
+            for (int j = 0; j < 4; ++j)
+              s[h][c + j] =
+                  (__uint_as_float(hi[c + j]) + __uint_as_float(lo[c + j])) * (ff[j] * kf);
           }
         }
         tc_fence_before();
-        if (tree && node >= 0) {
+        if (odd) {
 #pragma unroll
-          for (int c = 0; c < C; ++c)
-            if (node >= NODES || !((m.sees[wg * C + c] >> (node & 63)) & 1)) s[c] = -INFINITY;
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+              if (!((vis[h] >> c) & 1)) s[h][c] = -INFINITY;
+          }
         }
+        {
+          float w[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float w = warp_max(s[c]);
-          if (lane == c) top_mine = w;
+          for (int c = 0; c < C; ++c) w[c] = warp_max(fmaxf(s[0][c], s[1][c]));
+          if (lane == 0) {
+#pragma unroll
+            for (int c = 0; c < C; c += 4)
+              *reinterpret_cast<float4*>(&m.wmax[wg][wq][c]) =
+                  make_float4(w[c], w[c + 1], w[c + 2], w[c + 3]);
+          }
         }
         if (tree) {
           // the largest V exponent among what a row sees: one per row here
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < C; ++c) {
-            const uint32_t w = __reduce_max_sync(0xffffffffu, s[c] == -INFINITY ? 0u : ve);
-            if (lane == c) exp_mine = w;
+            const uint32_t w = __reduce_max_sync(
+                0xffffffffu, max((vis[0] >> c) & 1 ? ve[0] : 0u, (vis[1] >> c) & 1 ? ve[1] : 0u));
+            if (lane == 0) m.wexp[wg][wq][c] = w;
           }
-          if (lane < C) m.wexp[wg][lane][wq] = exp_mine;
         } else {
-          const uint32_t w = __reduce_max_sync(0xffffffffu, held ? ve : 0u);
+          const uint32_t w =
+              __reduce_max_sync(0xffffffffu, max(vis[0] ? ve[0] : 0u, vis[1] ? ve[1] : 0u));
           if (lane == 0) m.wtop[wg][wq] = w;
         }
-        if (lane < C) m.wmax[wg][lane][wq] = top_mine;
         dead = named_barrier_or(bar_wg, 128, !ok);
         if (dead) break;
         const uint32_t etop = tree ? 0u
@@ -703,13 +850,13 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
                                          max(m.wtop[wg][2], m.wtop[wg][3]));
         bool moved = false;
         if (lt < C) {
-          const float4 w4 = *reinterpret_cast<const float4*>(m.wmax[wg][lt]);
-          const float top = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w));
-          uint32_t e = etop;
+          const float top = fmaxf(fmaxf(m.wmax[wg][0][lt], m.wmax[wg][1][lt]),
+                                  fmaxf(m.wmax[wg][2][lt], m.wmax[wg][3][lt]));
+          uint32_t ex = etop;
           if (tree) {
-            const uint4 e4 = *reinterpret_cast<const uint4*>(m.wexp[wg][lt]);
-            e = max(max(e4.x, e4.y), max(e4.z, e4.w));
-            m.ecol[wg][lt] = e;
+            ex = max(max(m.wexp[wg][0][lt], m.wexp[wg][1][lt]),
+                     max(m.wexp[wg][2][lt], m.wexp[wg][3][lt]));
+            m.eh[wg][lt] = ex < 254u ? __uint_as_float((254u - ex) << 23) : __uint_as_float(1u << 22);
           }
           // a tile without a visible position changes nothing
           const float ref = top == -INFINITY ? (m_run == -INFINITY ? 0.f : m_run) : ceilf(top);
@@ -724,34 +871,43 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
           m.mref[wg][lt] = ref;
           m.alpha[wg][lt] = al;
           m.beta[wg][lt] = pow2i(d);
-          m.beta_o[wg][g & 1][lt] = pow2i(d + (int)e - 127);
+          m.beta_o[wg][g & 1][lt] = pow2i(d + (int)ex - 127);
         }
         const bool rescale = named_barrier_or(bar_wg, 128, moved);
         // weights; their sums per position in l, scaled to the running maximum
-        uint32_t ph[C / 2];
-        const float vf = tree ? 0.f : pow2i(min((int)ve - (int)etop, 0)) * WSCALE;
+        if (rescale) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) l[c] *= m.alpha[wg][c];
+        }
 #pragma unroll
         for (int c = 0; c < C; c += 4) {
           const float4 r4 = *reinterpret_cast<const float4*>(&m.mref[wg][c]);
           const float4 b4 = *reinterpret_cast<const float4*>(&m.beta[wg][c]);
           const float rr[4] = {r4.x, r4.y, r4.z, r4.w}, bb[4] = {b4.x, b4.y, b4.z, b4.w};
-          float p[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            p[j] = ta_exp2(s[c + j] - rr[j]);
-            if (rescale) l[c + j] *= m.alpha[wg][c + j];
-            l[c + j] = fmaf(p[j], bb[j], l[c + j]);
+            s[0][c + j] = ta_exp2(s[0][c + j] - rr[j]);
+            s[1][c + j] = ta_exp2(s[1][c + j] - rr[j]);
+            l[c + j] = fmaf(s[0][c + j] + s[1][c + j], bb[j], l[c + j]);
           }
+        }
+        // with the position's V scale, in fp16
+        uint32_t ph[2][C / 2];
+        float vf[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           if (tree) {
+            // 2^(ev - E of the row); above 1 only where the weight is 0
+            const float f = __uint_as_float(ve[h] << 23);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              p[j] *= pow2i(min((int)ve - (int)m.ecol[wg][c + j], 0)) * WSCALE;
+            for (int c = 0; c < C; ++c) s[h][c] *= fminf(f * m.eh[wg][c], 1.f);
+            vf[h] = WSCALE;
           } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] *= vf;
+            vf[h] = pow2i(min((int)ve[h] - (int)etop, 0)) * WSCALE;
           }
-          ph[c / 2] = pack_f16x2(p[0], p[1]);
-          ph[c / 2 + 1] = pack_f16x2(p[2], p[3]);
+#pragma unroll
+          for (int c = 0; c < C; c += 2)
+            ph[h][c / 2] = pack_f16x2(s[h][c] * vf[h], s[h][c + 1] * vf[h]);
         }
         // the tile before: its output, now that its product is done
         if (tile > first_tile) add_o(g - 1);
@@ -759,19 +915,55 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
 #pragma unroll
           for (int c = 0; c < C; ++c) acc[c] *= m.alpha[wg][c];
         }
-        // the weights' codes, 16 rows a store
+        if (odd && wg == 0) {
+          // V rows that must not reach the product: nothing held (stale
+          // bytes), or a node's NaN, which only the nodes that see it may get.
+          // Here the last tile's product is done, so its V tile has landed and the
+          // barriers' phases are unambiguous.
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t j = 2 * g + h;
+            ok = mbar_wait_warp(&m.v_full[j % VS], (j / VS) & 1, abort_flag, a.err) && ok;
+            const unsigned t = (unsigned)tile * TILE + h * SUB + lt;
+            uint4* vr = reinterpret_cast<uint4*>(sV + (j % VS) * F::KV_BYTES + lt * D);
+            if (t >= end || e[h * SUB] == 0 || e[TILE + h * SUB] == 0) {
 #pragma unroll
-        for (int c0 = 0; c0 < C; c0 += 16) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            split4(ph[c0 / 2 + 2 * i], ph[c0 / 2 + 2 * i + 1], &hi[i], &lo[i]);
-          *reinterpret_cast<uint4*>(sP + sw_off<2 * R>(lt, wg * C + c0)) =
-              make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(sP + sw_off<2 * R>(lt, R + wg * C + c0)) =
-              make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              for (int i = 0; i < D / 16; ++i) vr[i] = make_uint4(0, 0, 0, 0);
+            } else if (t >= pos) {
+              bool any = false;
+#pragma unroll 1
+              for (int i = 0; i < D / 16; ++i) {
+                const uint4 x = vr[i];
+                const uint32_t n[4] = {__vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
+                                       __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
+                                       __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
+                                       __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)};
+                if (n[0] | n[1] | n[2] | n[3]) {
+                  any = true;
+                  vr[i] = make_uint4(x.x & ~n[0], x.y & ~n[1], x.z & ~n[2], x.w & ~n[3]);
+                }
+              }
+              if (any) atomicOr(&m.nan_nodes, 1ull << (t - pos));
+            }
+          }
         }
-        // also orders this thread's reads of the stage before the next copy into it
+        // the weights' codes
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t hi[C / 4], lo[C / 4];
+#pragma unroll
+          for (int i = 0; i < C / 4; ++i) split4(ph[h][2 * i], ph[h][2 * i + 1], &hi[i], &lo[i]);
+          uint8_t* to_hi = sP + sw_off<2 * R>(h * SUB + lt, wg * C);
+          uint8_t* to_lo = sP + sw_off<2 * R>(h * SUB + lt, R + wg * C);
+          if constexpr (C == 16) {
+            *reinterpret_cast<uint4*>(to_hi) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(to_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint2*>(to_hi) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to_lo) = make_uint2(lo[0], lo[1]);
+          }
+        }
+        // also orders this thread's reads of the exponents before a later copy there
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&m.p_ready);
@@ -779,20 +971,37 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       // ---- the unit's last product, and what it leaves
       if (!dead) {
         add_o(g - 1);
+        // sums over the positions: through the place of the weights, which the
+        // last product is done with
+        float* ls = reinterpret_cast<float*>(sP) + wg * C * 128;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          float x = l[c];
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-          if (lane == 0) m.lsum[wg][c][wq] = x;
-        }
+        for (int c = 0; c < C; ++c) ls[c * 128 + lt] = l[c];
         if (lt < C) m.mref[wg][lt] = m_run;
         dead = named_barrier_or(bar_wg, 128, !ok);
+        const bool whole = u.first == 0 && u.stop == u.tiles;
+        float* part = a.parts + (size_t)(2 * cta + (u.first == 0)) * slot_floats(R, D) + R * D;
+#pragma unroll 1
+        for (int c = wq; c < C; c += 4) {
+          float x = (ls[c * 128 + lane] + ls[c * 128 + 32 + lane]) +
+                    (ls[c * 128 + 64 + lane] + ls[c * 128 + 96 + lane]);
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+          if (lane == 0) {
+            const int r = wg * C + c;
+            if (m.nan_row[r]) x = __uint_as_float(0x7FC00000u);
+            m.inv[r] = x == 0.f ? 0.f : 1.f / (x * WSCALE);
+            if (!whole && !dead) {
+              part[2 * r] = m.mref[wg][c];
+              part[2 * r + 1] = x;
+            }
+          }
+        }
+        named_barrier_sync(bar_wg, 128);
       }
-      if (!dead) finish_unit(first_tile, stop, drafts);
-      // all warpgroups are done with the unit's rows, or stop together
-      if (named_barrier_or(1, ALL, dead) || left <= 0) break;
-      cu.next_unit(a);
+      if (!dead) finish_unit(u);
+      // all warpgroups are done with the unit and its rows, or stop together
+      if (named_barrier_or(1, ALL, dead)) break;
+      if (th == 0) mbar_arrive(&m.u_empty[un % UNITS]);
     }
   }
   tc_fence_before();
@@ -803,52 +1012,79 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
   }
 }
 
-// Joins the parts of the units that lie in more than one run: one warp per
-// row, in run order.
-template <int D, int R>
-__global__ void __launch_bounds__(128) tree_attn_combine_kernel(const TreeArgs a) {
+// Joins the parts of the units that lie in more than one run, in run order:
+// one CTA of 8 warps per unit and 8 / WPR of its rows.
+template <int D, int R, int WPR>
+__global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a) {
   using namespace ta;
+  constexpr int V = D / 32;
+  __shared__ float part_o[8][D], part_l[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Head hd = a.heads[blockIdx.x];
-  if (hd.follow <= 0) return;
-  const int lane = threadIdx.x % 32, r = blockIdx.y * 4 + threadIdx.x / 32;
-  const int flat = hd.rb * R + r;
-  const int node = flat / a.G, h = hd.hk * a.G + flat % a.G;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int unit = blockIdx.x;
+  const int rb = unit % a.blocks, hk = unit / a.blocks % a.c.Hkv, b = unit / a.blocks / a.c.Hkv;
   bool bad;
-  const SeqRange sq = seq_range(a.s, hd.b, &bad);
-  if (node >= sq.count) return;
+  const SeqRange sq = seq_range(a.s, b, &bad);
+  // units of fewer nodes than N may not exist: their entry was not written
+  if (rb * R >= sq.count * a.G) return;
+  const Head hd = a.heads[unit];
+  if (hd.follow == 0) return;
+  const int r = blockIdx.y * (8 / WPR) + warp / WPR;
+  const int flat = rb * R + r, node = flat / a.G, h = hk * a.G + flat % a.G;
   const int n = hd.follow + 1;
-  // part i: slot 1 of this run, then slot 0 of the following ones
-  auto part = [&](int i) {
-    return a.parts + (size_t)(2 * (blockIdx.x + i) + (i == 0)) * slot_floats(R, D);
-  };
+  // part i: slot 1 of the first run, then slot 0 of the following ones
+  const float* base = a.parts + (size_t)2 * hd.run * slot_floats(R, D);
+  auto part = [&](int i) { return base + (size_t)(2 * i + (i == 0)) * slot_floats(R, D); };
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i)[R * D + 2 * r]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  constexpr int V = D / 32;
   float o[V], sum = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) o[j] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* p = part(i);
-    const float2 ml = *reinterpret_cast<const float2*>(p + R * D + 2 * r);
-    const float f = ml.x == -INFINITY ? 0.f : pow2i((int)fmaxf(ml.x - top, -200.f));
-    sum = fmaf(ml.y, f, sum);
-    float v[V];
-    if (V == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
-      v[0] = x.x; v[1] = x.y; v[2 % V] = x.z; v[3 % V] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(p + r * D + lane * 2);
-      v[0] = x.x; v[1] = x.y;
+  constexpr int U = 8;
+  for (int i0 = warp % WPR; i0 < n; i0 += WPR * U) {
+    float2 ml[U];
+    float v[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * WPR;
+      if (i >= n) continue;
+      const float* p = part(i);
+      ml[u] = *reinterpret_cast<const float2*>(p + R * D + 2 * r);
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
+        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(p + r * D + lane * 2);
+        v[u][0] = x.x; v[u][1] = x.y;
+      }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = fmaf(v[j], f, o[j]);
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * WPR >= n) continue;
+      const float f = ml[u].x == -INFINITY ? 0.f : pow2i((int)fmaxf(ml[u].x - top, -200.f));
+      sum = fmaf(ml[u].y, f, sum);
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = fmaf(v[u][j], f, o[j]);
+    }
   }
+  if (WPR > 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) part_o[warp][lane * V + j] = o[j];
+    if (lane == 0) part_l[warp] = sum;
+    __syncthreads();
+    if (warp % WPR != 0) return;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      sum += part_l[warp + w];
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] += part_o[warp + w][lane * V + j];
+    }
+  }
+  if (node >= sq.count) return;
   const float inv = sum == 0.f ? 0.f : 1.f / (sum * WSCALE);
-  uint16_t* dst = a.out + (((int64_t)hd.b * a.s.N + node) * a.Hq + h) * D + lane * V;
+  uint16_t* dst = a.out + (((int64_t)b * a.s.N + node) * a.Hq + h) * D + lane * V;
 #pragma unroll
   for (int j = 0; j < V; j += 2)
     *reinterpret_cast<uint32_t*>(dst + j) =
@@ -860,9 +1096,18 @@ static int tree_block_rows(int N, int G) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
+static int tree_blocks(int N, int G) {
+  const int R = tree_block_rows(N, G);
+  return (N * G + R - 1) / R;
+}
+static size_t tree_heads_bytes(const strata_kv_cache_t& c, const strata_kv_seqs_t& s, int Hq) {
+  const size_t units = (size_t)s.B * c.Hkv * tree_blocks(s.N, Hq / c.Hkv);
+  return (units * sizeof(ta::Head) + 255) & ~size_t(255);
+}
+
 size_t tree_attn_scratch(const strata_kv_cache_t& c, const strata_kv_seqs_t& s, int Hq) {
   const int R = tree_block_rows(s.N, Hq / c.Hkv);
-  return ((ta::MAX_CTAS * sizeof(ta::Head) + 255) & ~size_t(255)) +
+  return tree_heads_bytes(c, s, Hq) +
          (size_t)ta::MAX_CTAS * 2 * ta::slot_floats(R, c.D) * sizeof(float);
 }
 
@@ -870,7 +1115,7 @@ template <int D, int R>
 static cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                                cudaStream_t stream) {
   using F = ta::Cfg<D, R>;
-  constexpr int SMEM = F::MISC_OFF + (int)sizeof(ta::Misc<R, F::NWG, F::C, F::STAGES>);
+  constexpr int SMEM = F::MISC_OFF + (int)sizeof(ta::Misc<F, R>);
   static_assert(SMEM <= 232448, "shared memory");
   static_assert(F::CTAS == 1 || 2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, R>,
@@ -881,16 +1126,20 @@ static cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const C
   tree_attn_kernel<D, R><<<grid, F::THREADS, SMEM, stream>>>(mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // many parts per unit: a row's parts over 8 warps; few: a row per warp
+  const int units = a.s.B * a.c.Hkv * a.blocks;
+  const bool wide = grid / units >= 4;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, R / 4);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(units, wide ? R : R / 8);
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_attn_combine_kernel<D, R>, a);
+  return wide ? cudaLaunchKernelEx(&cfg, tree_attn_combine_kernel<D, R, 8>, a)
+              : cudaLaunchKernelEx(&cfg, tree_attn_combine_kernel<D, R, 1>, a);
 }
 
 cudaError_t launch_tree_attn(const strata_kv_cache_t& c, const strata_kv_seqs_t& s,
@@ -908,8 +1157,8 @@ cudaError_t launch_tree_attn(const strata_kv_cache_t& c, const strata_kv_seqs_t&
   a.scale = scale * 1.4426950408889634f;
   a.out = out;
   a.heads = static_cast<ta::Head*>(ws);
-  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
-                                     ((ta::MAX_CTAS * sizeof(ta::Head) + 255) & ~size_t(255)));
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + tree_heads_bytes(c, s, Hq));
+  a.blocks = tree_blocks(s.N, a.G);
   a.err = err;
   CUtensorMap mk, mv;
   const uint64_t rows = (uint64_t)c.pages * c.Hkv * c.page;
