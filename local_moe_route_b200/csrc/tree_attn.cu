@@ -70,23 +70,22 @@ struct Cfg {
   static constexpr int C = R == 16 ? TA_C16 : 16;      // row columns per softmax warpgroup
   static constexpr int NWG = R / C;
   static constexpr int CTAS = R == 64 ? 1 : 2;         // per SM
-  static constexpr int NS = R == 16 ? 2 : 1;           // score tiles in TMEM
   // K and V rings, in MMA tiles
-  static constexpr int KS = (R == 64 ? 4 : R == 32 ? 2 : 4) * (D == 64 ? 2 : 1);
+  static constexpr int KS = (R == 64 ? 4 : 2) * (D == 64 ? 2 : 1);
   static constexpr int VS = (R == 64 ? 4 : 2) * (D == 64 ? 2 : 1);
-  static constexpr int ES = KS / 2 + NS + 1;           // exponents, in softmax tiles
+  static constexpr int ES = KS / 2 + 2;                // exponents, in softmax tiles
   static constexpr int SOFT = NWG * 128;
   static constexpr int THREADS = SOFT + 64;
   static constexpr int KV_BYTES = SUB * D;             // one operand tile
   static constexpr int K_OFF = 0;
   static constexpr int V_OFF = K_OFF + KS * KV_BYTES;
   static constexpr int Q_OFF = V_OFF + VS * KV_BYTES;          // [2R][D] codes
-  static constexpr int P_OFF = Q_OFF + 2 * R * D;              // [TILE][2R] codes
+  static constexpr int QR_OFF = Q_OFF + 2 * R * D;             // [R][D] bf16, as they come
+  static constexpr int P_OFF = QR_OFF + 2 * R * D;             // [TILE][2R] codes
   static constexpr int E_OFF = P_OFF + TILE * 2 * R;           // [ES][K, V][TILE] exponents
   static constexpr int MISC_OFF = E_OFF + ES * 2 * TILE;
-  static constexpr int S_COLS = 4 * R;                 // TMEM: NS score tiles, one O tile
-  static constexpr int O_COL = NS * S_COLS;
-  static constexpr int TMEM_COLS = R == 64 ? 512 : 256;
+  static constexpr int O_COL = 4 * R;                  // TMEM: the scores, then O
+  static constexpr int TMEM_COLS = R == 64 ? 512 : R == 32 ? 256 : 128;
 };
 
 // One unit as a run sees it: tiles first .. stop - 1 of (sequence, KV head,
@@ -99,17 +98,20 @@ struct Unit {
 template <class F, int R>
 struct Misc {
   uint64_t k_full[F::KS], k_empty[F::KS], v_full[F::VS], v_empty[F::VS], e_full[F::ES];
-  uint64_t s_full[F::NS], p_ready, o_full, q_full, u_full[UNITS], u_empty[UNITS];
+  uint64_t s_full, s_free, p_ready, o_full, q_full, qr_full, qr_empty;
+  uint64_t u_full[UNITS], u_empty[UNITS];
   uint32_t seen_by[NODES][2];        // rows that see the node
   unsigned long long nan_nodes;      // nodes whose V holds a NaN
   Unit unit[UNITS];
   uint32_t tmem;
   int abort;
-  int parent[NODES];
+  int parent[UNITS][NODES];
+  int row[UNITS][R];                 // a row's node and query head: node * Hq + head
+  int row_node[UNITS][R];
   int64_t scan[F::THREADS / 32];
   int64_t start_off;
   int start_b;
-  int nan_row[R], node[R], head[R];
+  int nan_row[R];
   alignas(16) float qf[R];                       // score factor of the row
   alignas(16) float wmax[F::NWG][4][F::C];       // per warp: largest score of the tile
   alignas(16) uint32_t wexp[F::NWG][4][F::C];    // per warp: largest visible V exponent
@@ -117,6 +119,7 @@ struct Misc {
   alignas(16) float mref[F::NWG][F::C], beta[F::NWG][F::C], alpha[F::NWG][F::C];
   alignas(16) float beta_o[F::NWG][2][F::C];
   alignas(16) float eh[F::NWG][F::C];            // a row's V exponent as a factor
+  alignas(16) float lsum[F::NWG][4][F::C];       // per warp: sums of the weights
   alignas(16) float inv[R];                      // 1 / (sum * WSCALE)
 };
 
@@ -239,6 +242,38 @@ __device__ __forceinline__ void tmem_load2(uint32_t at0, uint32_t at1, uint32_t 
   }
 }
 
+// Pairs of fp32 values, one instruction for both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(uint32_t x, uint32_t y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ f32x2 pair(float x, float y) {
+  return pair(__float_as_uint(x), __float_as_uint(y));
+}
+__device__ __forceinline__ void unpair(f32x2 v, float& x, float& y) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  x = __uint_as_float(a);
+  y = __uint_as_float(b);
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 __device__ __forceinline__ float ta_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -331,7 +366,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
                      const __grid_constant__ CUtensorMap map_v, const TreeArgs a) {
   using namespace ta;
   using F = Cfg<D, R>;
-  constexpr int NWG = F::NWG, C = F::C, KS = F::KS, VS = F::VS, ES = F::ES, NS = F::NS;
+  constexpr int NWG = F::NWG, C = F::C, KS = F::KS, VS = F::VS, ES = F::ES;
   using M = Misc<F, R>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sK = smem + F::K_OFF;
@@ -356,7 +391,10 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       mbar_init(&m.v_empty[i], 1);
     }
     for (int i = 0; i < ES; ++i) mbar_init(&m.e_full[i], 1);
-    for (int i = 0; i < NS; ++i) mbar_init(&m.s_full[i], 1);
+    mbar_init(&m.s_full, 1);
+    mbar_init(&m.s_free, F::SOFT);
+    mbar_init(&m.qr_full, 1);
+    mbar_init(&m.qr_empty, 1);
     mbar_init(&m.p_ready, F::SOFT);
     mbar_init(&m.o_full, 1);
     mbar_init(&m.q_full, F::SOFT);
@@ -423,7 +461,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     // then V of the tile before it.
     Cursor<R> cu;
     cu.start(a, m.start_b, m.start_off, w1 - w0);
-    uint32_t jk = 0, jv = 0, g = 0, un = 0;
+    uint32_t jk = 0, jv = 0, g = 0, un = 0, nq = 0;
     int64_t row[2] = {-1, -1};         // of the tile, per MMA tile: this lane's page
     bool dead = false;
     const int page = a.c.page;
@@ -459,9 +497,9 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       }
       return true;
     };
-    // The slot's last tile is done with: this warp has waited for the K tile
-    // KS / 2 tiles back, whose scores were taken after the weights NS + KS / 2
-    // tiles back were finished.
+    // The slot's last tile is done with: this warp has waited until the K tile
+    // KS / 2 tiles back was read, which comes after the weights KS / 2 + 2 tiles
+    // back were finished.
     auto load_e = [&]() {
       const int es = g % ES;
       uint8_t* e = sE + es * 2 * TILE + lane * page;
@@ -495,6 +533,51 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         dead = true;
         break;
       }
+      if (some) {
+        // its rows, and their parents' nodes when the run reaches the tree
+        const bool drafts = (unsigned)u.stop * TILE > (unsigned)u.pos;
+        uint32_t n = 0;
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += 32) {
+          const int r = r0 + lane;
+          const int flat = u.rb * R + r, node = flat / a.G;
+          if (r < R) {
+            m.row_node[us][r] = node;
+            m.row[us][r] = node * a.Hq + u.hk * a.G + flat - node * a.G;
+          }
+          n += __popc(__ballot_sync(0xffffffffu, r < R && node < u.count));
+        }
+        if (drafts)
+#pragma unroll
+          for (int j = 0; j < NODES; j += 32) {
+            const int i = j + lane;
+            int p = -1;
+            if (i < u.count) {
+              p = a.parent ? a.parent[(int64_t)u.b * a.s.N + i] : i - 1;
+              if (p < -1 || p >= i) {
+                atomicOr(a.err, kErrIndex);
+                p = -1;
+              }
+            }
+            m.parent[us][i] = p;
+          }
+        if (un > 0 && !mbar_wait_warp(&m.qr_empty, (un - 1) & 1, abort_flag, a.err)) {
+          dead = true;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&m.qr_full, n * D * 2);
+        __syncwarp();
+#pragma unroll 1
+        for (int r = lane; r < R; r += 32) {
+          const int node = m.row_node[us][r], head = m.row[us][r] - node * a.Hq;
+          if (node < u.count)
+            bulk_load(smem + F::QR_OFF + r * D * 2,
+                      a.q + ((int64_t)u.b * a.s.N + node) * a.q_stride + (int64_t)head * D, D * 2,
+                      &m.qr_full);
+        }
+        ++nq;
+      }
+      __syncwarp();
       if (lane == 0) {
         if (some) m.unit[us] = u;
         m.unit[us].last = !some;       // an entry without tiles ends the run
@@ -548,6 +631,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       drain_ring<KS>(m.k_full, jk);
       drain_ring<VS>(m.v_full, jv);
       drain_ring<ES>(m.e_full, g);
+      drain_ring<1>(&m.qr_full, nq);
     }
   } else if (warp == W_MMA) {
     // ------------------------------------------------ MMA issue
@@ -564,11 +648,11 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         if (leader) {
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            mma_f8_ss(tmem + (i % NS) * F::S_COLS + h * 2 * R,
+            mma_f8_ss(tmem + h * 2 * R,
                       smem_desc(smem_addr(sK + ks * F::KV_BYTES) + 32 * k, 8 * D, sw_mode(D)),
                       smem_desc(smem_addr(sQ) + 32 * k, 8 * D, sw_mode(D)), ID_S, k > 0);
           mma_commit(&m.k_empty[ks]);
-          if (h == 1) mma_commit(&m.s_full[i % NS]);
+          if (h == 1) mma_commit(&m.s_full);
         }
         __syncwarp();
       }
@@ -608,15 +692,24 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       tc_fence_after();
       if (!scores(g)) break;
       for (int i = 0; i < tiles; ++i, ++g) {
-        const bool more = i + 1 < tiles;
-        // the next scores as early as their place in TMEM allows
-        if (NS == 2 && more && !scores(g + 1)) dead = true;
-        if (dead || !mbar_wait_warp(&m.p_ready, g & 1, abort_flag, a.err)) {
+        // the next scores as soon as these have left TMEM
+        if (i + 1 < tiles) {
+          if (!mbar_wait_warp(&m.s_free, g & 1, abort_flag, a.err)) {
+            dead = true;
+            break;
+          }
+          tc_fence_after();
+          if (!scores(g + 1)) {
+            dead = true;
+            break;
+          }
+        }
+        if (!mbar_wait_warp(&m.p_ready, g & 1, abort_flag, a.err)) {
           dead = true;
           break;
         }
         tc_fence_after();
-        if ((NS == 1 && more && !scores(g + 1)) || !output(g)) {
+        if (!output(g)) {
           dead = true;
           break;
         }
@@ -631,7 +724,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     // the feature whose sums this thread keeps (D = 64: 16 lanes per warp)
     const int feat = D == 128 ? lt : wq * 16 + lane;
     const bool has_feat = D == 128 || lane < 16;
-    float acc[C], l[C];
+    f32x2 acc[C / 2], l[C / 2];
     uint32_t g = 0;
     bool ok = true, dead = false;
 
@@ -645,17 +738,19 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
 #pragma unroll
       for (int c = 0; c < C; c += 4) {
         const float4 b4 = *reinterpret_cast<const float4*>(bo + c);
-        const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[c + j] =
-              fmaf(__uint_as_float(hi[c + j]) + __uint_as_float(lo[c + j]), bb[j], acc[c + j]);
+        acc[c / 2] = fma2(add2(pair(hi[c], hi[c + 1]), pair(lo[c], lo[c + 1])), pair(b4.x, b4.y),
+                          acc[c / 2]);
+        acc[c / 2 + 1] = fma2(add2(pair(hi[c + 2], hi[c + 3]), pair(lo[c + 2], lo[c + 3])),
+                              pair(b4.z, b4.w), acc[c / 2 + 1]);
       }
     };
 
     // The unit's results: rounded to the output when the run holds all of it,
     // its part otherwise.
-    auto finish_unit = [&](const Unit& u) {
+    auto finish_unit = [&](const Unit& u, int us) {
+      float o[C];
+#pragma unroll
+      for (int c = 0; c < C; c += 2) unpair(acc[c / 2], o[c], o[c + 1]);
       unsigned long long nan_nodes = (unsigned)u.stop * TILE > (unsigned)u.pos ? m.nan_nodes : 0;
       while (nan_nodes) {
         const int j = __ffsll((long long)nan_nodes) - 1;
@@ -665,71 +760,44 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         const uint32_t by = m.seen_by[j][wg * C / 32] >> (wg * C % 32);
 #pragma unroll
         for (int c = 0; c < C; ++c)
-          if (nan && ((by >> c) & 1)) acc[c] = __uint_as_float(0x7FC00000u);
-      }
-      const bool whole = u.first == 0 && u.stop == u.tiles;
-      if (u.first == 0 && th == 0) {
-        // the last run that holds a tile of this unit: the unit ends
-        // (tiles - stop) tiles behind this run
-        Head hd;
-        hd.run = cta;
-        hd.follow = whole ? 0 : (int)(((w1 + (u.tiles - u.stop)) * runs - 1) / total) - cta;
-        a.heads[((int64_t)u.b * a.c.Hkv + u.hk) * a.blocks + u.rb] = hd;
+          if (nan && ((by >> c) & 1)) o[c] = __uint_as_float(0x7FC00000u);
       }
       if (!has_feat) return;
-      if (whole) {
+      if (u.first == 0 && u.stop == u.tiles) {
         uint16_t* out = a.out + (int64_t)u.b * a.s.N * a.Hq * D + feat;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int r = wg * C + c;
-          if (m.node[r] < u.count)
-            out[(int64_t)(m.node[r] * a.Hq + m.head[r]) * D] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(acc[c] * m.inv[r]));
-        }
+        for (int c = 0; c < C; ++c)
+          if (m.row_node[us][wg * C + c] < u.count)
+            out[(int64_t)m.row[us][wg * C + c] * D] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(o[c] * m.inv[wg * C + c]));
       } else {
         float* part = a.parts + (size_t)(2 * cta + (u.first == 0)) * slot_floats(R, D) +
                       wg * C * D + feat;
 #pragma unroll
-        for (int c = 0; c < C; ++c) part[c * D] = acc[c];
+        for (int c = 0; c < C; ++c) part[c * D] = o[c];
       }
     };
 
     for (uint32_t un = 0;; ++un) {
       // ---- a unit begins: its query rows, split and scaled, and what they see
-      const Unit& u = m.unit[un % UNITS];
-      dead = !mbar_wait_warp(&m.u_full[un % UNITS], (un / UNITS) & 1, abort_flag, a.err);
+      const int us = un % UNITS;
+      const Unit& u = m.unit[us];
+      dead = !mbar_wait_warp(&m.u_full[us], (un / UNITS) & 1, abort_flag, a.err);
       if (named_barrier_or(1, ALL, dead)) break;
       if (u.last) break;
       const unsigned pos = (unsigned)u.pos;
       const bool drafts = (unsigned)u.stop * TILE > pos;     // the run reaches the tree
-      if (th < R) {
-        const int flat = u.rb * R + th;
-        m.node[th] = flat / a.G;
-        m.head[th] = u.hk * a.G + flat % a.G;
-      }
-      if (th < NODES && drafts) {
-        int p = -1;
-        if (th < u.count) {
-          p = a.parent ? a.parent[(int64_t)u.b * a.s.N + th] : th - 1;
-          if (p < -1 || p >= th) {
-            atomicOr(a.err, kErrIndex);
-            p = -1;
-          }
-        }
-        m.parent[th] = p;
-        m.seen_by[th][0] = m.seen_by[th][1] = 0;
-      }
+      if (th < NODES) m.seen_by[th][0] = m.seen_by[th][1] = 0;
       if (th == 0) m.nan_nodes = 0;
-      named_barrier_sync(1, ALL);
+      ok = mbar_wait_warp(&m.qr_full, un & 1, abort_flag, a.err) && ok;
       constexpr int LPR = D / 8;             // lanes per row, 8 values each
 #pragma unroll 1
       for (int r0 = 0; r0 < R; r0 += ALL / LPR) {
         const int r = r0 + th / LPR, ch = th % LPR;
         if (r0 + ALL / LPR > R && r >= R) continue;
-        const int node = m.node[r];
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (node < u.count)
-          x = ld_nc_v4(a.q + ((int64_t)u.b * a.s.N + node) * a.q_stride + m.head[r] * D + ch * 8);
+        if (m.row_node[us][r] < u.count)
+          x = *reinterpret_cast<const uint4*>(smem + F::QR_OFF + (r * D + ch * 8) * 2);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
         uint32_t top = 0;
 #pragma unroll
@@ -762,15 +830,19 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       }
       fence_proxy_async_smem();
       mbar_arrive(&m.q_full);
-      if (drafts && th < R)
-        for (int j = min(m.node[th], NODES - 1); j >= 0; j = m.parent[j])
-          atomicOr(&m.seen_by[j][th / 32], 1u << (th % 32));
-      named_barrier_sync(1, ALL);
+      dead = named_barrier_or(1, ALL, !ok);
+      if (!dead && drafts) {
+        if (th < R)
+          for (int j = min(m.row_node[us][th], NODES - 1); j >= 0; j = m.parent[us][j])
+            atomicOr(&m.seen_by[j][th / 32], 1u << (th % 32));
+        named_barrier_sync(1, ALL);
+      }
+      if (th == 0) mbar_arrive(&m.qr_empty);
 
       float m_run = -INFINITY;               // of column lt, in threads lt < C
 #pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] = l[c] = 0.f;
-      const int first_tile = u.first, stop = u.stop;
+      for (int c = 0; c < C / 2; ++c) acc[c] = l[c] = pair(0.f, 0.f);
+      const int first_tile = u.first, stop = dead ? u.first : u.stop;
       const unsigned end = u.end;
       for (int tile = first_tile; tile < stop; ++tile, ++g) {
         ok = mbar_wait_warp(&m.e_full[g % ES], (g / ES) & 1, abort_flag, a.err) && ok;
@@ -791,26 +863,27 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
               vis[h] = m.seen_by[t - pos][wg * C / 32] >> (wg * C % 32);
           }
         }
-        ok = mbar_wait_warp(&m.s_full[g % NS], (g / NS) & 1, abort_flag, a.err) && ok;
+        ok = mbar_wait_warp(&m.s_full, g & 1, abort_flag, a.err) && ok;
         tc_fence_after();
         float s[2][C];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float kf = __uint_as_float(ke[h] << 23);
+          const f32x2 kf = pair(ke[h] << 23, ke[h] << 23);
           uint32_t hi[C], lo[C];
-          const uint32_t col = lanes_at + (g % NS) * F::S_COLS + h * 2 * R;
-          tmem_load2<C>(col, col + R, hi, lo);
+          tmem_load2<C>(lanes_at + h * 2 * R, lanes_at + h * 2 * R + R, hi, lo);
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
             const float4 f4 = *reinterpret_cast<const float4*>(&m.qf[wg * C + c]);
-            const float ff[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              s[h][c + j] =
-                  (__uint_as_float(hi[c + j]) + __uint_as_float(lo[c + j])) * (ff[j] * kf);
+            unpair(mul2(add2(pair(hi[c], hi[c + 1]), pair(lo[c], lo[c + 1])),
+                        mul2(pair(f4.x, f4.y), kf)),
+                   s[h][c], s[h][c + 1]);
+            unpair(mul2(add2(pair(hi[c + 2], hi[c + 3]), pair(lo[c + 2], lo[c + 3])),
+                        mul2(pair(f4.z, f4.w), kf)),
+                   s[h][c + 2], s[h][c + 3]);
           }
         }
         tc_fence_before();
+        mbar_arrive(&m.s_free);
         if (odd) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -868,7 +941,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
           }
           const int d = now == -INFINITY ? 0 : (int)fmaxf(ref - now, -200.f);
           m_run = now;
-          m.mref[wg][lt] = ref;
+          m.mref[wg][lt] = -ref;
           m.alpha[wg][lt] = al;
           m.beta[wg][lt] = pow2i(d);
           m.beta_o[wg][g & 1][lt] = pow2i(d + (int)ex - 127);
@@ -877,18 +950,32 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         // weights; their sums per position in l, scaled to the running maximum
         if (rescale) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) l[c] *= m.alpha[wg][c];
+          for (int c = 0; c < C; c += 4) {
+            const float4 a4 = *reinterpret_cast<const float4*>(&m.alpha[wg][c]);
+            l[c / 2] = mul2(l[c / 2], pair(a4.x, a4.y));
+            l[c / 2 + 1] = mul2(l[c / 2 + 1], pair(a4.z, a4.w));
+          }
         }
 #pragma unroll
         for (int c = 0; c < C; c += 4) {
           const float4 r4 = *reinterpret_cast<const float4*>(&m.mref[wg][c]);
           const float4 b4 = *reinterpret_cast<const float4*>(&m.beta[wg][c]);
-          const float rr[4] = {r4.x, r4.y, r4.z, r4.w}, bb[4] = {b4.x, b4.y, b4.z, b4.w};
+          const f32x2 rr[2] = {pair(r4.x, r4.y), pair(r4.z, r4.w)};
+          const f32x2 bb[2] = {pair(b4.x, b4.y), pair(b4.z, b4.w)};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[0][c + j] = ta_exp2(s[0][c + j] - rr[j]);
-            s[1][c + j] = ta_exp2(s[1][c + j] - rr[j]);
-            l[c + j] = fmaf(s[0][c + j] + s[1][c + j], bb[j], l[c + j]);
+          for (int j = 0; j < 2; ++j) {
+            f32x2 p[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float x, y;
+              unpair(add2(pair(s[h][c + 2 * j], s[h][c + 2 * j + 1]), rr[j]), x, y);
+              x = ta_exp2(x);
+              y = ta_exp2(y);
+              p[h] = pair(x, y);
+              s[h][c + 2 * j] = x;
+              s[h][c + 2 * j + 1] = y;
+            }
+            l[c / 2 + j] = fma2(add2(p[0], p[1]), bb[j], l[c / 2 + j]);
           }
         }
         // with the position's V scale, in fp16
@@ -906,14 +993,21 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
             vf[h] = pow2i(min((int)ve[h] - (int)etop, 0)) * WSCALE;
           }
 #pragma unroll
-          for (int c = 0; c < C; c += 2)
-            ph[h][c / 2] = pack_f16x2(s[h][c] * vf[h], s[h][c + 1] * vf[h]);
+          for (int c = 0; c < C; c += 2) {
+            float x, y;
+            unpair(mul2(pair(s[h][c], s[h][c + 1]), pair(vf[h], vf[h])), x, y);
+            ph[h][c / 2] = pack_f16x2(x, y);
+          }
         }
         // the tile before: its output, now that its product is done
         if (tile > first_tile) add_o(g - 1);
         if (rescale) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) acc[c] *= m.alpha[wg][c];
+          for (int c = 0; c < C; c += 4) {
+            const float4 a4 = *reinterpret_cast<const float4*>(&m.alpha[wg][c]);
+            acc[c / 2] = mul2(acc[c / 2], pair(a4.x, a4.y));
+            acc[c / 2 + 1] = mul2(acc[c / 2 + 1], pair(a4.z, a4.w));
+          }
         }
         if (odd && wg == 0) {
           // V rows that must not reach the product: nothing held (stale
@@ -968,37 +1062,50 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         tc_fence_before();
         mbar_arrive(&m.p_ready);
       }
-      // ---- the unit's last product, and what it leaves
+      // ---- what the unit leaves: sums over the positions, the last product
       if (!dead) {
-        add_o(g - 1);
-        // sums over the positions: through the place of the weights, which the
-        // last product is done with
-        float* ls = reinterpret_cast<float*>(sP) + wg * C * 128;
+        float x[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) ls[c * 128 + lt] = l[c];
-        if (lt < C) m.mref[wg][lt] = m_run;
-        dead = named_barrier_or(bar_wg, 128, !ok);
-        const bool whole = u.first == 0 && u.stop == u.tiles;
-        float* part = a.parts + (size_t)(2 * cta + (u.first == 0)) * slot_floats(R, D) + R * D;
-#pragma unroll 1
-        for (int c = wq; c < C; c += 4) {
-          float x = (ls[c * 128 + lane] + ls[c * 128 + 32 + lane]) +
-                    (ls[c * 128 + 64 + lane] + ls[c * 128 + 96 + lane]);
+        for (int c = 0; c < C; c += 2) unpair(l[c / 2], x[c], x[c + 1]);
+        // over the warp's lanes: each step halves the columns a lane keeps
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-          if (lane == 0) {
-            const int r = wg * C + c;
-            if (m.nan_row[r]) x = __uint_as_float(0x7FC00000u);
-            m.inv[r] = x == 0.f ? 0.f : 1.f / (x * WSCALE);
-            if (!whole && !dead) {
-              part[2 * r] = m.mref[wg][c];
-              part[2 * r + 1] = x;
-            }
+        for (int w = C / 2, bit = 16; w > 0; w /= 2, bit /= 2) {
+#pragma unroll
+          for (int c = 0; c < w; ++c) {
+            const float give = lane & bit ? x[c] : x[c + w], keep = lane & bit ? x[c + w] : x[c];
+            x[c] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
           }
         }
+#pragma unroll
+        for (int bit = 16 / C; bit > 0; bit /= 2) x[0] += __shfl_xor_sync(0xffffffffu, x[0], bit);
+        if (lane % (32 / C) == 0) m.lsum[wg][wq][lane / (32 / C)] = x[0];
         named_barrier_sync(bar_wg, 128);
+        const bool whole = u.first == 0 && u.stop == u.tiles;
+        if (lt < C) {
+          const int r = wg * C + lt;
+          float sum = (m.lsum[wg][0][lt] + m.lsum[wg][1][lt]) +
+                      (m.lsum[wg][2][lt] + m.lsum[wg][3][lt]);
+          if (m.nan_row[r]) sum = __uint_as_float(0x7FC00000u);
+          m.inv[r] = sum == 0.f ? 0.f : 1.f / (sum * WSCALE);
+          if (!whole) {
+            float* part =
+                a.parts + (size_t)(2 * cta + (u.first == 0)) * slot_floats(R, D) + R * D + 2 * r;
+            part[0] = m_run;
+            part[1] = sum;
+          }
+        }
+        if (u.first == 0 && th == 64) {
+          // the last run that holds a tile of this unit: the unit ends
+          // (tiles - stop) tiles behind this run
+          Head hd;
+          hd.run = cta;
+          hd.follow = whole ? 0 : (int)(((w1 + (u.tiles - u.stop)) * runs - 1) / total) - cta;
+          a.heads[((int64_t)u.b * a.c.Hkv + u.hk) * a.blocks + u.rb] = hd;
+        }
+        add_o(g - 1);
+        dead = named_barrier_or(bar_wg, 128, !ok);
+        if (!dead) finish_unit(u, us);
       }
-      if (!dead) finish_unit(u);
       // all warpgroups are done with the unit and its rows, or stop together
       if (named_barrier_or(1, ALL, dead)) break;
       if (th == 0) mbar_arrive(&m.u_empty[un % UNITS]);
