@@ -16,37 +16,37 @@ namespace strata {
 
 namespace kvc {
 constexpr int THREADS = 256;
-constexpr int UNROLL = 2;    // rows in flight per thread group
+constexpr int WARPS = THREADS / 32;
 }  // namespace kvc
 
 __device__ __forceinline__ float pow2_biased(int biased) {   // 2^(biased - 127), biased in 1..254
   return __uint_as_float((uint32_t)biased << 23);
 }
 
-// Eight bf16 values per lane, D / 8 lanes per row: codes (8 bytes) and the
+// Sixteen bf16 values per lane, D / 16 lanes per row: codes (16 bytes) and the
 // row's biased exponent.
 template <int D>
-__device__ __forceinline__ uint2 quantise8(const uint4& x, int* biased) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ uint4 quantise16(const uint4& x0, const uint4& x1, int* biased) {
+  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
   // largest finite magnitude, as bf16 bits
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-    if (lo < 0x7F80u) top = max(top, lo);
-    if (hi < 0x7F80u) top = max(top, hi);
+    top = max(top, lo < 0x7F80u ? lo : 0u);
+    top = max(top, hi < 0x7F80u ? hi : 0u);
   }
 #pragma unroll
-  for (int off = D / 16; off > 0; off >>= 1)
+  for (int off = D / 32; off > 0; off >>= 1)
     top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
   // 448 = 1.75 * 2^8: mantissas above 1.75 take the next exponent
   int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
   e = min(max(e, -126), 119);
   *biased = e + 127;
   const float s = pow2_biased(127 - e);
-  uint32_t c[2];
+  uint32_t c[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 4; ++h) {
     c[h] = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -56,52 +56,89 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, int* biased) {
       c[h] |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * j);
     }
   }
-  return make_uint2(c[0], c[1]);
+  return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// One group of D / 8 lanes per row; rows in the order (token, head, K or V).
+// How the lanes of a warp share the rows of the call.  D / 16 lanes take a row
+// (16 values each), so a warp takes RPS = 512 / D rows at a time.  A token's
+// 2 * Hkv rows (K of every head, then V of every head) go to one warp in steps of
+// RPS; when they are fewer than RPS, several tokens share the warp.
+template <int D>
+struct RowLanes {
+  static constexpr int LPR = D / 16, RPS = 32 / LPR;
+  int ch, r, step;        // 16-value piece, first row, rows per step
+  int tok;                // the lane's token, -1: none
+  __device__ __forceinline__ RowLanes(const strata_kv_cache_t& c, const strata_kv_seqs_t& s) {
+    const int lane = threadIdx.x % 32, sub = lane / LPR, rows = 2 * c.Hkv;
+    const int warp = blockIdx.x * kvc::WARPS + threadIdx.x / 32;
+    const int tpw = rows < RPS ? RPS / rows : 1;
+    const int mine = rows < RPS ? sub / rows : 0;
+    ch = lane % LPR;
+    r = sub - mine * rows;
+    step = rows < RPS ? rows : RPS;
+    const int64_t t = (int64_t)warp * tpw + mine;
+    tok = mine < tpw && t < (int64_t)s.B * s.N ? (int)t : -1;
+  }
+  static int ctas(const strata_kv_cache_t& c, const strata_kv_seqs_t& s) {
+    const int rows = 2 * c.Hkv, tpw = rows < RPS ? RPS / rows : 1;
+    return (int)(((int64_t)s.B * s.N + kvc::WARPS * tpw - 1) / (kvc::WARPS * tpw));
+  }
+};
+
+// The position of token `tok` of the call, -1 when its slot is not in use.
+__device__ __forceinline__ int64_t token_pos(const strata_kv_seqs_t& s, int tok, int* b,
+                                             unsigned* err) {
+  if (tok < 0) return -1;
+  *b = tok / s.N;
+  const int i = tok - *b * s.N;
+  bool bad;
+  const SeqRange q = seq_range(s, *b, &bad);
+  if (bad) atomicOr(err, kErrIndex);
+  return i < q.count ? (int64_t)q.pos + i : -1;
+}
+
+// Bound by its bytes once there are tens of thousands of rows, by the chain
+// position -> page -> row below; two steps' loads are in flight while the page
+// is looked up (their addresses do not depend on it).  More tokens per
+// warp in place of more warps was slower (four 6144-token chunks, 8 rows a
+// token: 17.2, 19.0 and 19.3 us with 1, 2 and 4).
 template <int D>
 __global__ void __launch_bounds__(kvc::THREADS)
     kv_append_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, const uint16_t* __restrict__ k,
                      const uint16_t* __restrict__ v, int64_t stride, unsigned* err) {
-  constexpr int LPR = D / 8;                       // lanes per row
-  constexpr int GROUPS = kvc::THREADS / LPR;       // rows per CTA and step
-  const int lane = threadIdx.x % LPR;
-  const int rows = s.B * s.N * c.Hkv * 2;
-  // the whole CTA runs every step: the row maximum uses full-warp shuffles
-  for (int base = blockIdx.x * GROUPS * kvc::UNROLL; base < rows;
-       base += gridDim.x * GROUPS * kvc::UNROLL) {
-    uint4 x[kvc::UNROLL];
-    int64_t row[kvc::UNROLL];
-    bool is_v[kvc::UNROLL];
+  constexpr int U = 2;
+  const RowLanes<D> w(c, s);
+  int b = 0;
+  const int64_t pos = token_pos(s, w.tok, &b, err);
+  const int rows = 2 * c.Hkv;
+  int64_t row = -1;
+  for (int r0 = 0; r0 < rows; r0 += U * w.step) {
+    uint4 x[U][2];
 #pragma unroll
-    for (int u = 0; u < kvc::UNROLL; ++u) {
-      const int r = base + u * GROUPS + (int)threadIdx.x / LPR;
-      row[u] = -1;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (r >= rows) continue;
-      const int kv = r & 1, th = r >> 1, h = th % c.Hkv, tok = th / c.Hkv;
-      const int b = tok / s.N, i = tok % s.N;
-      bool bad;
-      const SeqRange q = seq_range(s, b, &bad);
-      if (bad) atomicOr(err, kErrIndex);
-      if (i >= q.count) continue;
-      row[u] = row_of(c, s, b, (int64_t)q.pos + i);
-      if (row[u] < 0) {
-        atomicOr(err, kErrIndex);
-        continue;
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * w.step + w.r;
+      x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+      if (r < rows && pos >= 0) {
+        const uint16_t* src = (r >= c.Hkv ? v + (int64_t)(r - c.Hkv) * D : k + (int64_t)r * D) +
+                              w.tok * stride + w.ch * 16;
+        x[u][0] = ld_nc_v4(src);
+        x[u][1] = ld_nc_v4(src + 8);
       }
-      row[u] += (int64_t)h * c.page;
-      is_v[u] = kv != 0;
-      x[u] = ld_nc_v4((kv ? v : k) + tok * stride + h * D + lane * 8);
+    }
+    if (r0 == 0 && pos >= 0) {
+      row = row_of(c, s, b, pos);
+      if (row < 0) atomicOr(err, kErrIndex);
     }
 #pragma unroll
-    for (int u = 0; u < kvc::UNROLL; ++u) {
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * w.step + w.r;
       int biased;
-      const uint2 code = quantise8<D>(x[u], &biased);
-      if (row[u] < 0) continue;
-      *reinterpret_cast<uint2*>((is_v[u] ? c.v : c.k) + row[u] * D + lane * 8) = code;
-      if (lane == 0) (is_v[u] ? c.v_exp : c.k_exp)[row[u]] = (uint8_t)biased;
+      const uint4 code = quantise16<D>(x[u][0], x[u][1], &biased);
+      if (r >= rows || row < 0) continue;
+      const bool is_v = r >= c.Hkv;
+      const int64_t at = row + (int64_t)(is_v ? r - c.Hkv : r) * c.page;
+      *reinterpret_cast<uint4*>((is_v ? c.v : c.k) + at * D + w.ch * 16) = code;
+      if (w.ch == 0) (is_v ? c.v_exp : c.k_exp)[at] = (uint8_t)biased;
     }
   }
 }
@@ -116,51 +153,47 @@ template <int D>
 __global__ void __launch_bounds__(kvc::THREADS)
     kv_read_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, uint16_t* __restrict__ k_out,
                    uint16_t* __restrict__ v_out, unsigned* err) {
-  constexpr int LPR = D / 8;
-  constexpr int GROUPS = kvc::THREADS / LPR;
-  const int lane = threadIdx.x % LPR;
-  const int rows = s.B * s.N * c.Hkv * 2;
-  for (int base = blockIdx.x * GROUPS * kvc::UNROLL; base < rows;
-       base += gridDim.x * GROUPS * kvc::UNROLL) {
-    uint2 code[kvc::UNROLL];
-    float f[kvc::UNROLL];
-    uint16_t* dst[kvc::UNROLL];
+  constexpr int U = 2;
+  const RowLanes<D> w(c, s);
+  int b = 0;
+  const int64_t pos = token_pos(s, w.tok, &b, err);
+  if (pos < 0) return;
+  const int64_t row = row_of(c, s, b, pos);
+  if (row < 0) atomicOr(err, kErrIndex);
+  const int rows = 2 * c.Hkv;
+  for (int r0 = 0; r0 < rows; r0 += U * w.step) {
+    uint4 code[U];
+    int e[U];
+    uint16_t* out[U];
 #pragma unroll
-    for (int u = 0; u < kvc::UNROLL; ++u) {
-      const int r = base + u * GROUPS + (int)threadIdx.x / LPR;
-      dst[u] = nullptr;
-      code[u] = make_uint2(0, 0);
-      f[u] = 0.f;
-      if (r >= rows) continue;
-      const int kv = r & 1, th = r >> 1, h = th % c.Hkv, tok = th / c.Hkv;
-      const int b = tok / s.N, i = tok % s.N;
-      uint16_t* out = kv ? v_out : k_out;
-      if (!out) continue;
-      bool bad;
-      const SeqRange q = seq_range(s, b, &bad);
-      if (bad) atomicOr(err, kErrIndex);
-      if (i >= q.count) continue;
-      dst[u] = out + ((int64_t)tok * c.Hkv + h) * D + lane * 8;
-      int64_t row = row_of(c, s, b, (int64_t)q.pos + i);
-      if (row < 0) {
-        atomicOr(err, kErrIndex);
-        continue;
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * w.step + w.r;
+      const bool is_v = r >= c.Hkv;
+      const int h = is_v ? r - c.Hkv : r;
+      out[u] = r < rows ? (is_v ? v_out : k_out) : nullptr;
+      code[u] = make_uint4(0, 0, 0, 0);
+      e[u] = 0;
+      if (out[u] && row >= 0) {
+        const int64_t at = row + (int64_t)h * c.page;
+        e[u] = (is_v ? c.v_exp : c.k_exp)[at];
+        code[u] = ld_nc_v4((is_v ? c.v : c.k) + at * D + w.ch * 16);
       }
-      row += (int64_t)h * c.page;
-      const int e = (kv ? c.v_exp : c.k_exp)[row];
-      if (e == 0) continue;                        // nothing held: zeros
-      code[u] = ld_nc_v2((kv ? c.v : c.k) + row * D + lane * 8);
-      f[u] = pow2_biased(e);
+      if (out[u]) out[u] += ((int64_t)w.tok * c.Hkv + h) * D + w.ch * 16;
     }
 #pragma unroll
-    for (int u = 0; u < kvc::UNROLL; ++u) {
-      if (!dst[u]) continue;
-      uint4 y;
-      y.x = dequantise2(code[u].x & 0xFFFFu, f[u]);
-      y.y = dequantise2(code[u].x >> 16, f[u]);
-      y.z = dequantise2(code[u].y & 0xFFFFu, f[u]);
-      y.w = dequantise2(code[u].y >> 16, f[u]);
-      *reinterpret_cast<uint4*>(dst[u]) = y;
+    for (int u = 0; u < U; ++u) {
+      if (!out[u]) continue;
+      if (e[u] == 0) code[u] = make_uint4(0, 0, 0, 0);         // nothing held: zeros
+      const float f = pow2_biased(e[u]);
+      const uint32_t x[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
+      uint32_t y[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] = dequantise2(x[i] & 0xFFFFu, f);
+        y[2 * i + 1] = dequantise2(x[i] >> 16, f);
+      }
+      reinterpret_cast<uint4*>(out[u])[0] = make_uint4(y[0], y[1], y[2], y[3]);
+      reinterpret_cast<uint4*>(out[u])[1] = make_uint4(y[4], y[5], y[6], y[7]);
     }
   }
 }
@@ -234,29 +267,26 @@ __global__ void __launch_bounds__(kvc::THREADS)
   if (threadIdx.x == 0) pos_out[b] = pos + n;
 }
 
-static int row_grid(const strata_kv_cache_t& c, const strata_kv_seqs_t& s) {
-  const int64_t rows = (int64_t)s.B * s.N * c.Hkv * 2;
-  const int per = kvc::THREADS / (c.D / 8) * kvc::UNROLL;
-  const int64_t ctas = (rows + per - 1) / per;
-  return (int)(ctas < 148 * 32 ? ctas : 148 * 32);
-}
-
 cudaError_t launch_kv_append(const strata_kv_cache_t& c, const strata_kv_seqs_t& s,
                              const uint16_t* k, const uint16_t* v, int64_t stride, unsigned* err,
                              cudaStream_t stream) {
   if (c.D == 128)
-    kv_append_kernel<128><<<row_grid(c, s), kvc::THREADS, 0, stream>>>(c, s, k, v, stride, err);
+    kv_append_kernel<128><<<RowLanes<128>::ctas(c, s), kvc::THREADS, 0, stream>>>(c, s, k, v,
+                                                                                  stride, err);
   else
-    kv_append_kernel<64><<<row_grid(c, s), kvc::THREADS, 0, stream>>>(c, s, k, v, stride, err);
+    kv_append_kernel<64><<<RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream>>>(c, s, k, v, stride,
+                                                                                err);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const strata_kv_cache_t& c, const strata_kv_seqs_t& s, uint16_t* k_out,
                            uint16_t* v_out, unsigned* err, cudaStream_t stream) {
   if (c.D == 128)
-    kv_read_kernel<128><<<row_grid(c, s), kvc::THREADS, 0, stream>>>(c, s, k_out, v_out, err);
+    kv_read_kernel<128><<<RowLanes<128>::ctas(c, s), kvc::THREADS, 0, stream>>>(c, s, k_out, v_out,
+                                                                                err);
   else
-    kv_read_kernel<64><<<row_grid(c, s), kvc::THREADS, 0, stream>>>(c, s, k_out, v_out, err);
+    kv_read_kernel<64><<<RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream>>>(c, s, k_out, v_out,
+                                                                              err);
   return cudaGetLastError();
 }
 

@@ -41,8 +41,12 @@ struct RestRow {
   const int* gone;      // rejected tokens of the node (q == nullptr)
   int n_gone;
 
+  __device__ __forceinline__ double rest(float pv, float qv) const {
+    const double r = fma(-c, (double)qv, (double)pv);
+    return r > 0.0 ? r : 0.0;
+  }
   __device__ __forceinline__ double one(float pv, float qv, int x) const {
-    if (q) return fmax((double)pv - c * (double)qv, 0.0);
+    if (q) return rest(pv, qv);
     for (int i = 0; i < n_gone; ++i)
       if (gone[i] == x) return 0.0;
     return (double)pv;
@@ -71,8 +75,15 @@ struct RestRow {
                                          double (&r)[4]) const {
     const int x0 = 4 * blk - shift;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      r[j] = x0 + j >= 0 && x0 + j < V ? one(pv[j], qv[j], x0 + j) : 0.0;
+    for (int j = 0; j < 4; ++j)      // (elements outside the row were loaded as 0)
+      r[j] = q ? rest(pv[j], qv[j]) : (double)pv[j];
+    if (!q)
+      for (int i = 0; i < n_gone; ++i) {
+        const int d = gone[i] - x0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (d == j) r[j] = 0.0;
+      }
   }
 };
 
@@ -83,26 +94,41 @@ __device__ __forceinline__ double warp_sum(double v) {
 }
 
 // Sum of blocks [b0, b1) by one warp, the same in every lane.
+template <bool Q>
 __device__ __forceinline__ double run_sum(const RestRow& row, int b0, int b1, int lane) {
-  constexpr int U = 4;
-  double sum = 0.0;
+  constexpr int U = 2;
+  double s0 = 0.0, s1 = 0.0;
+  auto add = [](double& s, double r) {
+    if (r > 0.0) s += r;
+  };
   for (int blk = b0 + lane; blk < b1; blk += 32 * U) {
     float pv[U][4], qv[U][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (blk + 32 * u < b1) row.load(blk + 32 * u, pv[u], qv[u]);
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (blk + 32 * u < b1) {
+      for (int j = 0; j < 4; ++j) pv[u][j] = qv[u][j] = 0.f;
+      if (blk + 32 * u < b1) row.load(blk + 32 * u, pv[u], qv[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (Q) {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          add(s0, fma(-row.c, (double)qv[u][j], (double)pv[u][j]));
+          add(s1, fma(-row.c, (double)qv[u][j + 1], (double)pv[u][j + 1]));
+        }
+      } else {
         double r[4];
         row.values(blk + 32 * u, pv[u], qv[u], r);
-        sum += (r[0] + r[1]) + (r[2] + r[3]);
+        s0 += r[0] + r[1];
+        s1 += r[2] + r[3];
       }
+    }
   }
-  return warp_sum(sum);
+  return warp_sum(s0 + s1);
 }
 
-__global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREADS)
+__global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREADS, 2)
     verify_kernel(const int32_t* __restrict__ tokens, const int32_t* __restrict__ parent,
                   const int32_t* __restrict__ count, const float* __restrict__ p,
                   const float* __restrict__ q, const float* __restrict__ u_accept,
@@ -119,7 +145,7 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
   __shared__ double sums[2][CLUSTER * WARPS];
   __shared__ int gone[NODES], nodes[NODES];
   __shared__ int tok_s[NODES], par_s[NODES];
-  __shared__ float u_s[NODES];
+  __shared__ float u_s[NODES], p_s[NODES], q_s[NODES];
   int n = count ? count[b] : N;
   if (n < 0 || n > N) {
     if (rank == 0 && threadIdx.x == 0) atomicOr(err, kErrIndex);
@@ -148,6 +174,15 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
     tok_s[i] = x;
     par_s[i] = pa;
     u_s[i] = u_accept[at];
+    // the token's own probabilities after its parent, should it be asked for
+    float pv = 0.f, qv = 1.f;
+    if (i > 0 && pa >= 0 && (unsigned)x < (unsigned)V) {
+      const int64_t px = ((int64_t)b * N + pa) * V + x;
+      pv = __ldg(p + px);
+      if (q) qv = __ldg(q + px);
+    }
+    p_s[i] = pv;
+    q_s[i] = qv;
   }
   cluster.sync();            // every CTA runs: its shared memory may be written from now on
 
@@ -160,7 +195,7 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
     const int per = (blocks + CLUSTER * WARPS - 1) / (CLUSTER * WARPS);
     const int w = rank * WARPS + warp;
     const int b0 = min(w * per, blocks), b1 = min(b0 + per, blocks);
-    const double s = run_sum(row, b0, b1, lane);
+    const double s = row.q ? run_sum<true>(row, b0, b1, lane) : run_sum<false>(row, b0, b1, lane);
     if (lane < CLUSTER) cluster.map_shared_rank(&sums[turn][0], lane)[w] = s;
     cluster.sync();
     double t = 0.0;
@@ -170,16 +205,18 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
 
   int cur = 0, n_path = 1, n_gone = 0;
   double c = 0.0, S = 1.0;
+  bool known = true;         // S is the sum of r
   auto row_at = [&]() {
     RestRow r;
     const int64_t off = ((int64_t)b * N + cur) * V;
     r.p = p + off;
-    r.q = q ? q + off : nullptr;
+    // nothing rejected yet: r is p, whatever q is
+    r.q = q && c != 0.0 ? q + off : nullptr;
     r.c = c;
     r.V = V;
     r.shift = (int)(off & 3);
     r.gone = gone;
-    r.n_gone = n_gone;
+    r.n_gone = q ? 0 : n_gone;
     return r;
   };
   if (threadIdx.x == 0) nodes[0] = 0;
@@ -187,10 +224,9 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
     if (par_s[i] != cur) continue;
     const int x = tok_s[i];
     if ((unsigned)x >= (unsigned)V) continue;
-    const RestRow row = row_at();
-    const float pv = __ldg(row.p + x), qv = q ? __ldg(row.q + x) : 1.f;
-    const double r = row.one(pv, qv, x);
-    if ((double)u_s[i] * (double)qv * S < r) {
+    if (!known) S = total(row_at());
+    known = true;
+    if ((double)u_s[i] * (double)q_s[i] * S < row_at().one(p_s[i], q_s[i], x)) {
       cur = i;
       c = 0.0;
       S = 1.0;
@@ -200,10 +236,10 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
       ++n_path;
     } else {
       c += S;
+      known = false;
       if (threadIdx.x == 0) gone[n_gone] = x;
       ++n_gone;
       __syncthreads();
-      S = total(row_at());
     }
   }
   // the next token
@@ -212,25 +248,40 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
   const double sum = total(row);
   const double want = (double)u_sample[b] * sum;
   // the run that holds it: the first whose running sum exceeds `want`, else
-  // the last with a positive sum
-  int run = -1, last = -1;
-  double below = 0.0, below_run = 0.0, below_last = 0.0;
-  for (int i = 0; i < CLUSTER * WARPS; ++i) {
-    const double s = sums[turn][i];
-    if (s > 0.0) {
-      last = i;
-      below_last = below;
-    }
-    if (run < 0 && below + s > want) {
-      run = i;
-      below_run = below;
-    }
-    below += s;
+  // the last with a positive sum.  Every warp scans the sums, four to a lane.
+  constexpr int RPL = CLUSTER * WARPS / 32;
+  double mine[RPL], upto = 0.0;
+#pragma unroll
+  for (int j = 0; j < RPL; ++j) {
+    mine[j] = sums[turn][lane * RPL + j];
+    upto += mine[j];
   }
-  if (run < 0) {
-    run = last;
-    below_run = below_last;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double o = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += o;
   }
+  double at = __shfl_up_sync(0xffffffffu, upto, 1);
+  if (lane == 0) at = 0.0;
+  int hit = -1, last = -1;
+  double hit_at = 0.0, last_at = 0.0;
+#pragma unroll
+  for (int j = 0; j < RPL; ++j) {
+    if (mine[j] > 0.0) {
+      last = lane * RPL + j;
+      last_at = at;
+      if (hit < 0 && at + mine[j] > want) {
+        hit = last;
+        hit_at = at;
+      }
+    }
+    at += mine[j];
+  }
+  const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0);
+  const unsigned some = __ballot_sync(0xffffffffu, last >= 0);
+  const int from = hits ? __ffs(hits) - 1 : some ? 31 - __clz(some) : 0;
+  int run = __shfl_sync(0xffffffffu, hits ? hit : last, from);
+  const double below_run = __shfl_sync(0xffffffffu, hits ? hit_at : last_at, from);
   if (run < 0) {
     run = 0;
     if (rank == 0 && threadIdx.x == 0) atomicOr(err, kErrIndex);
@@ -239,38 +290,53 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
     const int blocks = (row.shift + V + 3) / 4;
     const int per = (blocks + CLUSTER * WARPS - 1) / (CLUSTER * WARPS);
     const int b0 = min(run * per, blocks), b1 = min(b0 + per, blocks);
+    // each lane takes a contiguous share, U blocks of it at a time
+    constexpr int U = 4;
     int found = -1, fallback = -1;
     double base = below_run;
-    for (int k0 = b0; k0 < b1 && found < 0; k0 += 32) {
-      const int blk = k0 + lane;
-      double r[4] = {0.0, 0.0, 0.0, 0.0};
-      if (blk < b1) {
-        float pv[4], qv[4];
-        row.load(blk, pv, qv);
-        row.values(blk, pv, qv, r);
-      }
-      const double mine = (r[0] + r[1]) + (r[2] + r[3]);
-      double upto = mine;                        // sum of lanes 0 .. lane
+    for (int k0 = b0; k0 < b1 && found < 0; k0 += 32 * U) {
+      const int share = min(U, (b1 - k0 + 31) / 32);
+      const int l0 = k0 + lane * share;
+      float pv[U][4], qv[U][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < share && l0 + u < b1) row.load(l0 + u, pv[u], qv[u]);
+      double mine_sum = 0.0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < share && l0 + u < b1) {
+          double r[4];
+          row.values(l0 + u, pv[u], qv[u], r);
+          mine_sum += (r[0] + r[1]) + (r[2] + r[3]);
+        }
+      double to = mine_sum;                      // sum of lanes 0 .. lane
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += o;
+        const double o = __shfl_up_sync(0xffffffffu, to, off);
+        if (lane >= off) to += o;
       }
-      const double before = __shfl_up_sync(0xffffffffu, upto, 1);
+      const double before = __shfl_up_sync(0xffffffffu, to, 1);
       double run_at = base + (lane ? before : 0.0);
-      int hit = -1, pos = -1;
+      int x_hit = -1, x_pos = -1;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        run_at += r[j];
-        const int x = 4 * blk - row.shift + j;
-        if (r[j] > 0.0) pos = x;
-        if (hit < 0 && r[j] > 0.0 && run_at > want) hit = x;
-      }
-      const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0);
-      const unsigned some = __ballot_sync(0xffffffffu, pos >= 0);
-      if (some) fallback = __shfl_sync(0xffffffffu, pos, 31 - __clz(some));
-      if (hits) found = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
-      base += __shfl_sync(0xffffffffu, upto, 31);
+      for (int u = 0; u < U; ++u)
+        if (u < share && l0 + u < b1) {
+          double r[4];
+          row.values(l0 + u, pv[u], qv[u], r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            run_at += r[j];
+            if (r[j] > 0.0) {
+              x_pos = 4 * (l0 + u) - row.shift + j;
+              if (x_hit < 0 && run_at > want) x_hit = x_pos;
+            }
+          }
+        }
+      const unsigned x_hits = __ballot_sync(0xffffffffu, x_hit >= 0);
+      const unsigned x_some = __ballot_sync(0xffffffffu, x_pos >= 0);
+      if (x_some) fallback = __shfl_sync(0xffffffffu, x_pos, 31 - __clz(x_some));
+      if (x_hits) found = __shfl_sync(0xffffffffu, x_hit, __ffs(x_hits) - 1);
+      base += __shfl_sync(0xffffffffu, to, 31);
     }
     if (found < 0) found = fallback < 0 ? 0 : fallback;
     for (int i = lane; i < N; i += 32) {

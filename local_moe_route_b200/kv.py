@@ -31,17 +31,32 @@ class _Refused(Exception):
     """A tensor argument the entry point would misread."""
 
 
+_torch = None      # torch, imported with the first tensor that is checked
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _dev(t: Any, dtype: str, elements: Optional[int] = None) -> Optional[int]:
     """Pointer of a dense tensor of the current device with the given type (and
     number of elements); None and raw pointers pass."""
     if t is None or isinstance(t, int):
         return t
-    import torch
-    if t.dtype is not getattr(torch, dtype) or not t.is_contiguous() or not t.is_cuda \
-            or t.get_device() != torch.cuda.current_device() \
-            or (elements is not None and t.numel() != elements):
+    torch = _torch or _load_torch()
+    if t.dtype is not getattr(torch, dtype) or not t.is_contiguous() \
+            or (elements is not None and t.numel() != elements) \
+            or t.get_device() != _device():
         raise _Refused
     return t.data_ptr()
+
+
+def _device() -> int:
+    """Index of the current CUDA device; -2 without one (a host tensor's is -1)."""
+    return _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -2
 
 
 def _rows(t: Any, B: int, N: int, heads: int, D: int):
@@ -49,19 +64,33 @@ def _rows(t: Any, B: int, N: int, heads: int, D: int):
     token are dense, the tokens follow each other at one stride."""
     if t is None or isinstance(t, int):
         return t, 0
-    import torch
-    if t.dtype is not torch.bfloat16 or not t.is_cuda or tuple(t.shape) != (B, N, heads, D) \
-            or t.get_device() != torch.cuda.current_device():
+    torch = _torch or _load_torch()
+    if t.dtype is not torch.bfloat16 or t.shape != (B, N, heads, D) \
+            or t.get_device() != _device():
         raise _Refused
-    st = t.stride()
-    if st[3] != 1 or (heads > 1 and st[2] != D):
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    sb, sn, sh, sd = t.stride()
+    if sd != 1 or (heads > 1 and sh != D):
         raise _Refused
-    step = st[1] if N > 1 else st[0] if B > 1 else 0
-    if N > 1 and B > 1 and st[0] != N * st[1]:
-        raise _Refused
-    if step < heads * D and B * N > 1:
+    step = sn if N > 1 else sb if B > 1 else 0
+    if (N > 1 and B > 1 and sb != N * sn) or (step < heads * D and B * N > 1):
         raise _Refused
     return t.data_ptr(), step
+
+
+def _here(*descriptors: Any) -> None:
+    """Refuses descriptors whose tensors are not on the current device."""
+    for d in descriptors:
+        if d.device is not None and d.device != _device():
+            raise _Refused
+
+
+def _on(stream: Any) -> Optional[int]:
+    """The stream's handle; None = the current stream of the current device."""
+    if stream is None and _torch is not None and _torch.cuda.is_initialized():
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+    return _stream(stream)
 
 
 class KvCache(ctypes.Structure):
@@ -70,6 +99,7 @@ class KvCache(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_int32), ("page", ctypes.c_int32), ("Hkv", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p)]
+    device = None      # of the tensors; None: raw pointers
 
     @classmethod
     def of(cls, k: Any, v: Any, k_exp: Any, v_exp: Any) -> "KvCache":
@@ -80,7 +110,7 @@ class KvCache(ctypes.Structure):
                     _dev(k_exp, "uint8", rows), _dev(v_exp, "uint8", rows))
         except _Refused:
             raise StrataError(STRATA_ERR_INVALID_ARG, "KvCache") from None
-        c.tensors = (k, v, k_exp, v_exp)
+        c.tensors, c.device = (k, v, k_exp, v_exp), k.get_device()
         return c
 
     @classmethod
@@ -97,6 +127,7 @@ class KvSeqs(ctypes.Structure):
     int32 or None (N)."""
     _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("table", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("count", ctypes.c_void_p)]
+    device = None
 
     @classmethod
     def of(cls, table: Any, pos: Any, count: Any = None, N: int = 1) -> "KvSeqs":
@@ -106,7 +137,7 @@ class KvSeqs(ctypes.Structure):
                     _dev(count, "int32", B))
         except _Refused:
             raise StrataError(STRATA_ERR_INVALID_ARG, "KvSeqs") from None
-        s.tensors = (table, pos, count)
+        s.tensors, s.device = (table, pos, count), table.get_device()
         return s
 
 
@@ -150,31 +181,34 @@ def strata_kv_append(cache: KvCache, seqs: KvSeqs, k, v, stride: int = 0, stream
     """k, v [B][N][Hkv][D] bf16; tensors may be parts of wider rows (their token
     stride is taken from them, `stride` is for raw pointers)."""
     try:
+        _here(cache, seqs)
         kp, ks = _rows(k, seqs.B, seqs.N, cache.Hkv, cache.D)
         vp, vs = _rows(v, seqs.B, seqs.N, cache.Hkv, cache.D)
     except _Refused:
         return STRATA_ERR_INVALID_ARG
     if ks != vs:
         return STRATA_ERR_INVALID_ARG
-    return _lib().strata_kv_append(cache, seqs, kp, vp, ks or int(stride), _stream(stream))
+    return (_bound or _lib()).strata_kv_append(cache, seqs, kp, vp, ks or int(stride), _on(stream))
 
 
 def strata_kv_read(cache: KvCache, seqs: KvSeqs, k_out, v_out, stream=None) -> int:
     n = seqs.B * seqs.N * cache.Hkv * cache.D
     try:
+        _here(cache, seqs)
         kp, vp = _dev(k_out, "bfloat16", n), _dev(v_out, "bfloat16", n)
     except _Refused:
         return STRATA_ERR_INVALID_ARG
-    return _lib().strata_kv_read(cache, seqs, kp, vp, _stream(stream))
+    return (_bound or _lib()).strata_kv_read(cache, seqs, kp, vp, _on(stream))
 
 
 def strata_kv_commit(cache: KvCache, seqs: KvSeqs, path, path_len, pos_out, stream=None) -> int:
     try:
+        _here(cache, seqs)
         a = (_dev(path, "int32", seqs.B * seqs.N), _dev(path_len, "int32", seqs.B),
              _dev(pos_out, "int32", seqs.B))
     except _Refused:
         return STRATA_ERR_INVALID_ARG
-    return _lib().strata_kv_commit(cache, seqs, *a, _stream(stream))
+    return (_bound or _lib()).strata_kv_commit(cache, seqs, *a, _on(stream))
 
 
 def strata_tree_attention_workspace_bytes(cache: KvCache, seqs: KvSeqs, Hq: int) -> int:
@@ -197,6 +231,7 @@ def strata_tree_attention(cache: KvCache, seqs: KvSeqs, parent, q, scale, out, w
     part of wider rows.  Hq and q_stride are for raw pointers."""
     B, N, D = seqs.B, seqs.N, cache.D
     try:
+        _here(cache, seqs)
         if not isinstance(q, int) and q is not None:
             Hq = int(q.shape[2]) if q.dim() == 4 else 0
         heads = int(Hq or 0)
@@ -205,9 +240,9 @@ def strata_tree_attention(cache: KvCache, seqs: KvSeqs, parent, q, scale, out, w
         wp = _dev(ws, "uint8")
     except _Refused:
         return STRATA_ERR_INVALID_ARG
-    return _lib().strata_tree_attention(
+    return (_bound or _lib()).strata_tree_attention(
         cache, seqs, pp, qp, qs or int(q_stride), heads, float(scale), op, wp,
-        _nbytes(ws) if ws_bytes is None else int(ws_bytes), _stream(stream))
+        _nbytes(ws) if ws_bytes is None else int(ws_bytes), _on(stream))
 
 
 def strata_verify_drafts(tokens, parent, count, p, q, u_accept, u_sample, dims, path, path_len,
@@ -222,4 +257,4 @@ def strata_verify_drafts(tokens, parent, count, p, q, u_accept, u_sample, dims, 
              _dev(out_tokens, "int32", nodes)]
     except _Refused:
         return STRATA_ERR_INVALID_ARG
-    return _lib().strata_verify_drafts(*a, d, *o, _stream(stream))
+    return (_bound or _lib()).strata_verify_drafts(*a, d, *o, _on(stream))
