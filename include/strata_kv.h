@@ -170,7 +170,7 @@ STRATA_API strata_status_t strata_verify_drafts(const int32_t* tokens, const int
  *            writes it; an entry outside [i, N) is reported and its row not moved
  *   path_len [B] int32; outside 0 .. N is reported and counts as 0
  *   pos_out  [B] int32 out: pos[b] + path_len[b]; may be pos itself
- * seqs.count is not used. */
+ * seqs.count is not used; B <= 65535. */
 STRATA_API strata_status_t strata_kv_commit(strata_kv_cache_t cache, strata_kv_seqs_t seqs,
                                  const int32_t* path, const int32_t* path_len,
                                  int32_t* pos_out, strata_stream_t stream);

@@ -142,7 +142,7 @@ strata_status_t strata_kv_commit(strata_kv_cache_t cache, strata_kv_seqs_t seqs,
                                  strata_stream_t stream) {
   const strata_status_t st = check_both(cache, seqs);
   if (st != STRATA_OK) return st;
-  if (seqs.N > STRATA_TREE_MAX_NODES) return STRATA_ERR_UNSUPPORTED;
+  if (seqs.N > STRATA_TREE_MAX_NODES || seqs.B > 65535) return STRATA_ERR_UNSUPPORTED;
   if (seqs.B == 0) return STRATA_OK;
   if (!ok_ptr(path) || !ok_ptr(path_len) || !ok_ptr(pos_out)) return STRATA_ERR_INVALID_ARG;
   unsigned* err = check_word();
