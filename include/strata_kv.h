@@ -105,7 +105,9 @@ STRATA_API strata_status_t strata_kv_read(strata_kv_cache_t cache, strata_kv_seq
  *            is reported and counts as -1.
  *   q        node i of sequence b at (b * N + i) * q_stride: [Hq][D] bf16
  *   q_stride elements, Hq * D or more, a multiple of 8; 0 = Hq * D
- *   Hq       query heads, Hq % Hkv == 0, Hq / Hkv <= 64, B * N * Hq < 2^30
+ *   Hq       query heads, Hq % Hkv == 0, Hq / Hkv <= 64, B * N * Hq < 2^30, and
+ *            B * Hkv * ceil(N * Hq / Hkv / 16) * (max_pages * page / 256 + 4)
+ *            < 2^31
  *   scale    <= 0 means 1 / sqrt(D)
  *   out      [B][N][Hq][D] bf16; rows of slots behind count[b] are left as they
  *            were; a node that sees no row gets zeros

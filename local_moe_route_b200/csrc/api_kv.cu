@@ -59,6 +59,10 @@ strata_status_t check_tree_dims(const strata_kv_cache_t& c, const strata_kv_seqs
   if (Hq <= 0 || Hq % c.Hkv) return STRATA_ERR_INVALID_ARG;
   if (s.N > STRATA_TREE_MAX_NODES || Hq / c.Hkv > 64 || (int64_t)s.B * s.N * Hq >= (1 << 30))
     return STRATA_ERR_UNSUPPORTED;
+  // the attention counts its tiles (and rows in blocks of 16 at least) in 31 bits
+  const int64_t blocks = ((int64_t)s.N * (Hq / c.Hkv) + 15) / 16;
+  if ((double)s.B * c.Hkv * blocks * ((double)s.max_pages * c.page / 256 + 4) >= 2147483648.0)
+    return STRATA_ERR_UNSUPPORTED;
   return STRATA_OK;
 }
 

@@ -15,10 +15,6 @@
 
 namespace strata {
 
-#ifndef MV_T
-#define MV_T 1024
-#define MV_H 8
-#endif
 namespace kvc {
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;

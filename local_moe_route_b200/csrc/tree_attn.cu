@@ -58,7 +58,7 @@ namespace ta {
 constexpr int SUB = 128;                    // positions per MMA tile
 constexpr int TILE = 2 * SUB;               // positions per softmax step
 constexpr int NODES = STRATA_TREE_MAX_NODES;
-constexpr int MAX_CTAS = 148 * 4;           // runs the workspace has room for
+constexpr int MAX_CTAS = 148 * 2;           // CTAs the workspace has room for
 constexpr float WSCALE = 448.f;             // weights are scaled to e4m3's largest value
 // What a unit costs besides its tiles (its query rows, the tree's masks, its
 // results), in tiles: units take that much more of the line.
@@ -91,8 +91,10 @@ struct Cfg {
 // One unit as a run sees it: tiles first .. stop - 1 of (sequence, KV head,
 // block of rows).
 struct Unit {
-  int b, hk, rb, pos, count, tiles, first, stop, last;
+  int b, hk, rb, pos, count, tiles, first, stop;
   unsigned end;              // positions with a column in the page table
+  int run, follow;           // the run, and how many runs after it go on with the unit
+  int last;                  // no unit: the CTA is done
 };
 
 template <class F, int R>
@@ -108,8 +110,8 @@ struct Misc {
   int parent[UNITS][NODES];
   int row[UNITS][R];                 // a row's node and query head: node * Hq + head
   int row_node[UNITS][R];
-  int64_t scan[F::THREADS / 32];
-  int64_t start_off;
+  uint32_t scan[F::THREADS / 32];
+  uint32_t start_off;
   int start_b;
   int nan_row[R];
   alignas(16) float qf[R];                       // score factor of the row
@@ -152,8 +154,8 @@ struct TreeArgs {
 struct TreeSeq {
   int pos, count, tiles, blocks;
   unsigned end;           // positions with a column in the page table
-  __device__ __forceinline__ int64_t length(const TreeArgs& a) const {   // in the line
-    return tiles ? (int64_t)(tiles + ta::UNIT_COST) * blocks * a.c.Hkv : 0;
+  __device__ __forceinline__ uint32_t length(const TreeArgs& a) const {   // in the line
+    return tiles ? (uint32_t)(tiles + ta::UNIT_COST) * (uint32_t)(blocks * a.c.Hkv) : 0u;
   }
 };
 
@@ -176,6 +178,23 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool repor
   return t;
 }
 
+// How the line of `total` places is cut into runs: one per CTA, no shorter than
+// a unit's cost and a tile.
+struct Line {
+  uint32_t total, runs, q, rem;
+  __device__ __forceinline__ Line(uint32_t n, uint32_t ctas) {
+    const uint32_t most = (n + ta::UNIT_COST) / (ta::UNIT_COST + 1);
+    total = n;
+    runs = most < ctas ? most : ctas;
+    q = runs ? n / runs : 0;
+    rem = n - q * runs;
+  }
+  __device__ __forceinline__ uint32_t start(uint32_t r) const { return r * q + min(r, rem); }
+  __device__ __forceinline__ uint32_t run_of(uint32_t w) const {
+    return w < rem * (q + 1) ? w / (q + 1) : rem + (w - rem * (q + 1)) / q;
+  }
+};
+
 // The units of a run in order.  A unit takes UNIT_COST + tiles places of the
 // line; a run that holds only its first places leaves all its tiles to
 // the next run.
@@ -183,16 +202,18 @@ template <int R>
 struct Cursor {
   TreeSeq t;
   int b, hk, rb;
-  int64_t off;            // place in the unit
-  int64_t left;           // places left in the run
-  __device__ __forceinline__ void start(const TreeArgs& a, int b0, int64_t o, int64_t n) {
+  uint32_t off;           // place in the unit
+  uint32_t at, left;      // place in the line; places left in the run
+  __device__ __forceinline__ void start(const TreeArgs& a, int b0, uint32_t o, uint32_t w,
+                                        uint32_t n) {
     b = b0;
+    at = w;
     left = n;
     t = tree_seq<R>(a, b, false);
-    const int64_t len = t.tiles + ta::UNIT_COST, u = o / len;
-    off = o % len;
-    rb = (int)(u % t.blocks);
+    const uint32_t len = t.tiles + ta::UNIT_COST, u = o / len;
+    off = o - u * len;
     hk = (int)(u / t.blocks);
+    rb = (int)u - hk * t.blocks;
   }
   __device__ __forceinline__ void advance(const TreeArgs& a) {
     off = 0;
@@ -205,20 +226,32 @@ struct Cursor {
       t = tree_seq<R>(a, b, false);
     } while (t.tiles == 0);
   }
-  // The next unit with tiles in this run; false when there is none.
-  __device__ __forceinline__ bool next(const TreeArgs& a, ta::Unit* u) {
+  // The next unit with tiles in run `run`; false when there is none.
+  __device__ __forceinline__ bool next(const TreeArgs& a, const Line& line, int run, ta::Unit* u) {
     while (left > 0) {
-      const int64_t len = t.tiles + ta::UNIT_COST;
-      const int64_t upto = min(len, off + left);
-      const int first = (int)max((int64_t)0, off - ta::UNIT_COST);
-      const int stop = (int)max((int64_t)0, upto - ta::UNIT_COST);
-      const ta::Unit x = {b, hk, rb, t.pos, t.count, t.tiles, first, stop, 0, t.end};
+      const uint32_t len = t.tiles + ta::UNIT_COST;
+      const uint32_t upto = min(len, off + left);
+      const int first = max(0, (int)off - ta::UNIT_COST);
+      const int stop = max(0, (int)upto - ta::UNIT_COST);
+      u->b = b;
+      u->hk = hk;
+      u->rb = rb;
+      u->pos = t.pos;
+      u->count = t.count;
+      u->tiles = t.tiles;
+      u->first = first;
+      u->stop = stop;
+      u->end = t.end;
+      u->run = run;
+      u->follow = upto == len ? 0 : (int)line.run_of(at + (len - off) - 1) - run;
+      u->last = 0;
+      at += upto - off;
       left -= upto - off;
-      if (left > 0) advance(a);
-      if (stop > first) {
-        *u = x;
-        return true;
-      }
+      if (left > 0)
+        advance(a);
+      else
+        off = upto;
+      if (stop > first) return true;
     }
     return false;
   }
@@ -411,38 +444,35 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
   }
   if (warp == W_MMA) tmem_alloc(&m.tmem, F::TMEM_COLS);
 
-  // ---- the line and this CTA's run of it: sequences in contiguous shares per
-  // thread, their lengths scanned over the CTA
+  // ---- the line: sequences in contiguous shares per thread, their lengths
+  // scanned over the CTA
   const int per = (a.s.B + F::THREADS - 1) / F::THREADS;
   const int sb0 = min(th * per, a.s.B), sb1 = min(sb0 + per, a.s.B);
-  int64_t mine = 0;
+  uint32_t mine = 0;
   for (int b = sb0; b < sb1; ++b) mine += tree_seq<R>(a, b, reporter).length(a);
-  int64_t incl = mine;
+  uint32_t incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+    const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += o;
   }
   if (lane == 31) m.scan[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int64_t before = incl - mine, total = 0;
+  uint32_t before = incl - mine, total = 0;
   for (int w = 0; w < F::THREADS / 32; ++w) {
     if (w < warp) before += m.scan[w];
     total += m.scan[w];
   }
-  // no run shorter than a unit's cost and a tile
-  const int64_t most = (total + UNIT_COST) / (UNIT_COST + 1);
-  const int64_t runs = most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x;
+  const Line line(total, gridDim.x);
   const int cta = blockIdx.x;
-  const bool active = cta < runs;
-  const int64_t w0 = active ? total * cta / runs : 0;
-  const int64_t w1 = active ? total * (cta + 1) / runs : 0;
+  const bool active = cta < (int)line.runs;
+  const uint32_t w0 = active ? line.start(cta) : 0;
   if (active && w0 >= before && w0 < before + mine) {
-    int64_t at = before;
+    uint32_t at = before;
     for (int b = sb0; b < sb1; ++b) {
-      const int64_t n = tree_seq<R>(a, b, false).length(a);
+      const uint32_t n = tree_seq<R>(a, b, false).length(a);
       if (w0 < at + n) {
         m.start_b = b;
         m.start_off = w0 - at;
@@ -460,7 +490,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     // In the order in which the places come free: exponents and K of a tile,
     // then V of the tile before it.
     Cursor<R> cu;
-    cu.start(a, m.start_b, m.start_off, w1 - w0);
+    cu.start(a, m.start_b, m.start_off, w0, line.start(cta + 1) - w0);
     uint32_t jk = 0, jv = 0, g = 0, un = 0, nq = 0;
     int64_t row[2] = {-1, -1};         // of the tile, per MMA tile: this lane's page
     bool dead = false;
@@ -524,68 +554,69 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         }
       ++g;
     };
-    while (!dead) {
-      Unit u;
-      const bool some = cu.next(a, &u);
+    // Tells the other warps of unit u (or that there is none left): its rows, the
+    // nodes' parents when the run reaches the tree, the rows' values.
+    auto announce = [&](const Unit& u, bool some) -> bool {
       const int us = un % UNITS;
       if (un >= (uint32_t)UNITS &&
-          !mbar_wait_warp(&m.u_empty[us], (un / UNITS - 1) & 1, abort_flag, a.err)) {
-        dead = true;
-        break;
-      }
+          !mbar_wait_warp(&m.u_empty[us], (un / UNITS - 1) & 1, abort_flag, a.err))
+        return false;
       if (some) {
-        // its rows, and their parents' nodes when the run reaches the tree
         const bool drafts = (unsigned)u.stop * TILE > (unsigned)u.pos;
         uint32_t n = 0;
+        int node[(R + 31) / 32], row_q[(R + 31) / 32];
 #pragma unroll
-        for (int r0 = 0; r0 < R; r0 += 32) {
-          const int r = r0 + lane;
-          const int flat = u.rb * R + r, node = flat / a.G;
+        for (int k = 0; k < (R + 31) / 32; ++k) {
+          const int r = k * 32 + lane, flat = u.rb * R + r;
+          node[k] = flat / a.G;
+          row_q[k] = node[k] * a.Hq + u.hk * a.G + flat - node[k] * a.G;
           if (r < R) {
-            m.row_node[us][r] = node;
-            m.row[us][r] = node * a.Hq + u.hk * a.G + flat - node * a.G;
+            m.row_node[us][r] = node[k];
+            m.row[us][r] = row_q[k];
           }
-          n += __popc(__ballot_sync(0xffffffffu, r < R && node < u.count));
+          if (r >= R) node[k] = u.count;
+          n += __popc(__ballot_sync(0xffffffffu, node[k] < u.count));
         }
-        if (drafts)
+        int up[NODES / 32];
 #pragma unroll
-          for (int j = 0; j < NODES; j += 32) {
-            const int i = j + lane;
-            int p = -1;
-            if (i < u.count) {
-              p = a.parent ? a.parent[(int64_t)u.b * a.s.N + i] : i - 1;
-              if (p < -1 || p >= i) {
-                atomicOr(a.err, kErrIndex);
-                p = -1;
-              }
-            }
-            m.parent[us][i] = p;
-          }
-        if (un > 0 && !mbar_wait_warp(&m.qr_empty, (un - 1) & 1, abort_flag, a.err)) {
-          dead = true;
-          break;
+        for (int j = 0; j < NODES / 32; ++j) {
+          const int i = j * 32 + lane;
+          up[j] = i < u.count ? i - 1 : -1;
+          if (drafts && a.parent && i < u.count) up[j] = a.parent[(int64_t)u.b * a.s.N + i];
         }
+        if (un > 0 && !mbar_wait_warp(&m.qr_empty, (un - 1) & 1, abort_flag, a.err)) return false;
         if (lane == 0) mbar_arrive_expect_tx(&m.qr_full, n * D * 2);
         __syncwarp();
-#pragma unroll 1
-        for (int r = lane; r < R; r += 32) {
-          const int node = m.row_node[us][r], head = m.row[us][r] - node * a.Hq;
-          if (node < u.count)
-            bulk_load(smem + F::QR_OFF + r * D * 2,
-                      a.q + ((int64_t)u.b * a.s.N + node) * a.q_stride + (int64_t)head * D, D * 2,
-                      &m.qr_full);
-        }
         ++nq;
+#pragma unroll
+        for (int k = 0; k < (R + 31) / 32; ++k)
+          if (node[k] < u.count)
+            bulk_load(smem + F::QR_OFF + (k * 32 + lane) * D * 2,
+                      a.q + ((int64_t)u.b * a.s.N + node[k]) * a.q_stride +
+                          (int64_t)(row_q[k] - node[k] * a.Hq) * D,
+                      D * 2, &m.qr_full);
+#pragma unroll
+        for (int j = 0; j < NODES / 32; ++j) {
+          const int i = j * 32 + lane;
+          if (up[j] < -1 || up[j] >= i) {
+            if (i < u.count) atomicOr(a.err, kErrIndex);
+            up[j] = -1;
+          }
+          m.parent[us][i] = up[j];
+        }
       }
       __syncwarp();
       if (lane == 0) {
         if (some) m.unit[us] = u;
-        m.unit[us].last = !some;       // an entry without tiles ends the run
+        m.unit[us].last = !some;
         mbar_arrive(&m.u_full[us]);
       }
       __syncwarp();
       ++un;
-      if (!some) break;
+      return true;
+    };
+    Unit u;
+    while (!dead && cu.next(a, line, cta, &u)) {
       for (int tile = u.first; tile < u.stop; ++tile) {
         int64_t now[2];
 #pragma unroll
@@ -614,6 +645,11 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
           dead = true;
           break;
         }
+        // (the unit's first copies are on their way before it is announced)
+        if (tile == u.first && !announce(u, true)) {
+          dead = true;
+          break;
+        }
         if (g > 1) {
           row[0] = was[0];
           row[1] = was[1];
@@ -626,6 +662,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         }
       }
     }
+    if (!dead) dead = !announce(Unit(), false);
     if (!dead && g > 0) dead = !load_v();
     if (dead) {
       drain_ring<KS>(m.k_full, jk);
@@ -771,7 +808,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
             out[(int64_t)m.row[us][wg * C + c] * D] =
                 __bfloat16_as_ushort(__float2bfloat16_rn(o[c] * m.inv[wg * C + c]));
       } else {
-        float* part = a.parts + (size_t)(2 * cta + (u.first == 0)) * slot_floats(R, D) +
+        float* part = a.parts + (size_t)(2 * u.run + (u.first == 0)) * slot_floats(R, D) +
                       wg * C * D + feat;
 #pragma unroll
         for (int c = 0; c < C; ++c) part[c * D] = o[c];
@@ -1089,17 +1126,15 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
           m.inv[r] = sum == 0.f ? 0.f : 1.f / (sum * WSCALE);
           if (!whole) {
             float* part =
-                a.parts + (size_t)(2 * cta + (u.first == 0)) * slot_floats(R, D) + R * D + 2 * r;
+                a.parts + (size_t)(2 * u.run + (u.first == 0)) * slot_floats(R, D) + R * D + 2 * r;
             part[0] = m_run;
             part[1] = sum;
           }
         }
         if (u.first == 0 && th == 64) {
-          // the last run that holds a tile of this unit: the unit ends
-          // (tiles - stop) tiles behind this run
           Head hd;
-          hd.run = cta;
-          hd.follow = whole ? 0 : (int)(((w1 + (u.tiles - u.stop)) * runs - 1) / total) - cta;
+          hd.run = u.run;
+          hd.follow = u.follow;
           a.heads[((int64_t)u.b * a.c.Hkv + u.hk) * a.blocks + u.rb] = hd;
         }
         add_o(g - 1);
@@ -1120,44 +1155,71 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
 }
 
 // Joins the parts of the units that lie in more than one run, in run order:
-// one CTA of 8 warps per unit and 8 / WPR of its rows.
+// one CTA of 8 warps per unit and 8 / WPR of its rows.  With few units
+// (WPR = 8) the CTA works out the unit's runs itself while the first kernel
+// is still busy; with many it reads them.
 template <int D, int R, int WPR>
-__global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a, uint32_t ctas) {
   using namespace ta;
-  constexpr int V = D / 32;
-  __shared__ float part_o[8][D], part_l[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int V = D / 32, U = 8;
+  __shared__ float part_o[8][D], part_l[8], part_m[8];
+  __shared__ uint32_t scan[8];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int unit = blockIdx.x;
   const int rb = unit % a.blocks, hk = unit / a.blocks % a.c.Hkv, b = unit / a.blocks / a.c.Hkv;
-  bool bad;
-  const SeqRange sq = seq_range(a.s, b, &bad);
-  // units of fewer nodes than N may not exist: their entry was not written
-  if (rb * R >= sq.count * a.G) return;
-  const Head hd = a.heads[unit];
+  const TreeSeq t = tree_seq<R>(a, b, false);
+  Head hd = {0, 0};
+  if (WPR > 1) {
+    // places below sequence b, and of all sequences
+    uint32_t below = 0, all = 0;
+    for (int i = threadIdx.x; i < a.s.B; i += 256) {
+      const uint32_t n = tree_seq<R>(a, i, false).length(a);
+      all += n;
+      if (i < b) below += n;
+    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    below = __reduce_add_sync(0xffffffffu, below);
+    if (lane == 0) {
+      scan[warp] = all;
+      part_l[warp] = __uint_as_float(below);
+    }
+    __syncthreads();
+    all = below = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      all += scan[w];
+      below += __float_as_uint(part_l[w]);
+    }
+    __syncthreads();
+    const Line line(all, ctas);
+    const uint32_t at = below + (uint32_t)(hk * t.blocks + rb) * (t.tiles + UNIT_COST) + UNIT_COST;
+    if (rb < t.blocks) {
+      hd.run = (int)line.run_of(at);
+      hd.follow = (int)line.run_of(at + t.tiles - 1) - hd.run;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // units of fewer nodes than N may not exist
+  if (rb >= t.blocks) return;
+  if (WPR == 1) hd = a.heads[unit];
   if (hd.follow == 0) return;
   const int r = blockIdx.y * (8 / WPR) + warp / WPR;
   const int flat = rb * R + r, node = flat / a.G, h = hk * a.G + flat % a.G;
   const int n = hd.follow + 1;
   // part i: slot 1 of the first run, then slot 0 of the following ones
   const float* base = a.parts + (size_t)2 * hd.run * slot_floats(R, D);
-  auto part = [&](int i) { return base + (size_t)(2 * i + (i == 0)) * slot_floats(R, D); };
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i)[R * D + 2 * r]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  float o[V], sum = 0.f;
+  float o[V], sum = 0.f, top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < V; ++j) o[j] = 0.f;
-  constexpr int U = 8;
   for (int i0 = warp % WPR; i0 < n; i0 += WPR * U) {
     float2 ml[U];
-    float v[U][V];
+    float v[U][V], most = top;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * WPR;
+      ml[u] = make_float2(-INFINITY, 0.f);
       if (i >= n) continue;
-      const float* p = part(i);
+      const float* p = base + (size_t)(2 * i + (i == 0)) * slot_floats(R, D);
       ml[u] = *reinterpret_cast<const float2*>(p + R * D + 2 * r);
       if constexpr (V == 4) {
         const float4 x = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
@@ -1167,6 +1229,13 @@ __global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a
         v[u][0] = x.x; v[u][1] = x.y;
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) most = fmaxf(most, ml[u].x);
+    const float keep = top == -INFINITY ? 0.f : pow2i((int)fmaxf(top - most, -200.f));
+    top = most;
+    sum *= keep;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] *= keep;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i0 + u * WPR >= n) continue;
@@ -1179,17 +1248,27 @@ __global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a
   if (WPR > 1) {
 #pragma unroll
     for (int j = 0; j < V; ++j) part_o[warp][lane * V + j] = o[j];
-    if (lane == 0) part_l[warp] = sum;
+    if (lane == 0) {
+      part_l[warp] = sum;
+      part_m[warp] = top;
+    }
     __syncthreads();
     if (warp % WPR != 0) return;
 #pragma unroll
-    for (int w = 1; w < WPR; ++w) {
-      sum += part_l[warp + w];
+    for (int w = 1; w < WPR; ++w) top = fmaxf(top, part_m[warp + w]);
+    sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) o[j] += part_o[warp + w][lane * V + j];
+    for (int j = 0; j < V; ++j) o[j] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      const float pm = part_m[warp + w];
+      const float f = pm == -INFINITY ? 0.f : pow2i((int)fmaxf(pm - top, -200.f));
+      sum = fmaf(part_l[warp + w], f, sum);
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = fmaf(part_o[warp + w][lane * V + j], f, o[j]);
     }
   }
-  if (node >= sq.count) return;
+  if (node >= t.count) return;
   const float inv = sum == 0.f ? 0.f : 1.f / (sum * WSCALE);
   uint16_t* dst = a.out + (((int64_t)b * a.s.N + node) * a.Hq + h) * D + lane * V;
 #pragma unroll
@@ -1203,6 +1282,12 @@ static int tree_block_rows(int N, int G) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
+// CTAs on `sms` SMs, as many as the workspace has room for at most.
+static int tree_ctas(int R, int sms) {
+  const int n = sms * (R == 64 ? 1 : 2);
+  const int room = ta::MAX_CTAS / (R == 64 ? 2 : 1);
+  return n < room ? n : room;
+}
 static int tree_blocks(int N, int G) {
   const int R = tree_block_rows(N, G);
   return (N * G + R - 1) / R;
@@ -1215,7 +1300,7 @@ static size_t tree_heads_bytes(const strata_kv_cache_t& c, const strata_kv_seqs_
 size_t tree_attn_scratch(const strata_kv_cache_t& c, const strata_kv_seqs_t& s, int Hq) {
   const int R = tree_block_rows(s.N, Hq / c.Hkv);
   return tree_heads_bytes(c, s, Hq) +
-         (size_t)ta::MAX_CTAS * 2 * ta::slot_floats(R, c.D) * sizeof(float);
+         (size_t)tree_ctas(R, ta::MAX_CTAS) * 2 * ta::slot_floats(R, c.D) * sizeof(float);
 }
 
 template <int D, int R>
@@ -1228,8 +1313,7 @@ static cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const C
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, R>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  int grid = sm_count() * F::CTAS;
-  if (grid > ta::MAX_CTAS) grid = ta::MAX_CTAS;
+  const int grid = tree_ctas(R, sm_count());
   tree_attn_kernel<D, R><<<grid, F::THREADS, SMEM, stream>>>(mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1245,8 +1329,8 @@ static cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const C
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, tree_attn_combine_kernel<D, R, 8>, a)
-              : cudaLaunchKernelEx(&cfg, tree_attn_combine_kernel<D, R, 1>, a);
+  return wide ? cudaLaunchKernelEx(&cfg, tree_attn_combine_kernel<D, R, 8>, a, (uint32_t)grid)
+              : cudaLaunchKernelEx(&cfg, tree_attn_combine_kernel<D, R, 1>, a, (uint32_t)grid);
 }
 
 cudaError_t launch_tree_attn(const strata_kv_cache_t& c, const strata_kv_seqs_t& s,
