@@ -48,12 +48,6 @@
 
 namespace strata {
 
-#ifndef TA_C16
-#define TA_C16 16
-#endif
-#ifndef TA_OV
-#define TA_OV 2
-#endif
 namespace ta {
 constexpr int SUB = 128;                    // positions per MMA tile
 constexpr int TILE = 2 * SUB;               // positions per softmax step
@@ -61,13 +55,20 @@ constexpr int NODES = STRATA_TREE_MAX_NODES;
 constexpr int MAX_CTAS = 148 * 2;           // CTAs the workspace has room for
 constexpr float WSCALE = 448.f;             // weights are scaled to e4m3's largest value
 // What a unit costs besides its tiles (its query rows, the tree's masks, its
-// results), in tiles: units take that much more of the line.
-constexpr int UNIT_COST = TA_OV;
+// results), in tiles: units take that much more of the line.  On short lines
+// the number of tiles per CTA counts, not their even cost.
+__host__ __device__ constexpr uint32_t unit_cost(uint32_t tiles, uint32_t ctas) {
+  return tiles >= 16 * ctas ? 3 : tiles >= 4 * ctas ? 2 : tiles > ctas ? 1 : 0;
+}
 constexpr int UNITS = 4;                    // units announced ahead
+#ifndef TA_C16
+#define TA_C16 16
+#endif
+constexpr int C16 = TA_C16;
 
 template <int D, int R>
 struct Cfg {
-  static constexpr int C = R == 16 ? TA_C16 : 16;      // row columns per softmax warpgroup
+  static constexpr int C = R == 16 ? C16 : 16;         // row columns per softmax warpgroup
   static constexpr int NWG = R / C;
   static constexpr int CTAS = R == 64 ? 1 : 2;         // per SM
   // K and V rings, in MMA tiles
@@ -110,7 +111,7 @@ struct Misc {
   int parent[UNITS][NODES];
   int row[UNITS][R];                 // a row's node and query head: node * Hq + head
   int row_node[UNITS][R];
-  uint32_t scan[F::THREADS / 32];
+  uint2 scan[F::THREADS / 32];
   uint32_t start_off;
   int start_b;
   int nan_row[R];
@@ -154,8 +155,8 @@ struct TreeArgs {
 struct TreeSeq {
   int pos, count, tiles, blocks;
   unsigned end;           // positions with a column in the page table
-  __device__ __forceinline__ uint32_t length(const TreeArgs& a) const {   // in the line
-    return tiles ? (uint32_t)(tiles + ta::UNIT_COST) * (uint32_t)(blocks * a.c.Hkv) : 0u;
+  __device__ __forceinline__ uint32_t units(const TreeArgs& a) const {
+    return tiles ? (uint32_t)(blocks * a.c.Hkv) : 0u;
   }
 };
 
@@ -178,16 +179,16 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool repor
   return t;
 }
 
-// How the line of `total` places is cut into runs: one per CTA, no shorter than
-// a unit's cost and a tile.
+// The line of all units' tiles, each unit with its cost in front, and how it is
+// cut into runs, one per CTA.
 struct Line {
-  uint32_t total, runs, q, rem;
-  __device__ __forceinline__ Line(uint32_t n, uint32_t ctas) {
-    const uint32_t most = (n + ta::UNIT_COST) / (ta::UNIT_COST + 1);
-    total = n;
-    runs = most < ctas ? most : ctas;
-    q = runs ? n / runs : 0;
-    rem = n - q * runs;
+  uint32_t cost, total, runs, q, rem;
+  __device__ __forceinline__ Line(uint32_t tiles, uint32_t units, uint32_t ctas) {
+    cost = ta::unit_cost(tiles, ctas);
+    total = tiles + cost * units;
+    runs = min(tiles, ctas);
+    q = runs ? total / runs : 0;
+    rem = total - q * runs;
   }
   __device__ __forceinline__ uint32_t start(uint32_t r) const { return r * q + min(r, rem); }
   __device__ __forceinline__ uint32_t run_of(uint32_t w) const {
@@ -195,22 +196,24 @@ struct Line {
   }
 };
 
-// The units of a run in order.  A unit takes UNIT_COST + tiles places of the
+// The units of a run in order.  A unit takes cost + tiles places of the
 // line; a run that holds only its first places leaves all its tiles to
 // the next run.
 template <int R>
 struct Cursor {
   TreeSeq t;
   int b, hk, rb;
+  int cost;
   uint32_t off;           // place in the unit
   uint32_t at, left;      // place in the line; places left in the run
-  __device__ __forceinline__ void start(const TreeArgs& a, int b0, uint32_t o, uint32_t w,
-                                        uint32_t n) {
+  __device__ __forceinline__ void start(const TreeArgs& a, const Line& line, int b0, uint32_t o,
+                                        uint32_t w, uint32_t n) {
     b = b0;
+    cost = (int)line.cost;
     at = w;
     left = n;
     t = tree_seq<R>(a, b, false);
-    const uint32_t len = t.tiles + ta::UNIT_COST, u = o / len;
+    const uint32_t len = t.tiles + cost, u = o / len;
     off = o - u * len;
     hk = (int)(u / t.blocks);
     rb = (int)u - hk * t.blocks;
@@ -229,10 +232,10 @@ struct Cursor {
   // The next unit with tiles in run `run`; false when there is none.
   __device__ __forceinline__ bool next(const TreeArgs& a, const Line& line, int run, ta::Unit* u) {
     while (left > 0) {
-      const uint32_t len = t.tiles + ta::UNIT_COST;
+      const uint32_t len = t.tiles + cost;
       const uint32_t upto = min(len, off + left);
-      const int first = max(0, (int)off - ta::UNIT_COST);
-      const int stop = max(0, (int)upto - ta::UNIT_COST);
+      const int first = max(0, (int)off - cost);
+      const int stop = max(0, (int)upto - cost);
       u->b = b;
       u->hk = hk;
       u->rb = rb;
@@ -448,31 +451,48 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
   // scanned over the CTA
   const int per = (a.s.B + F::THREADS - 1) / F::THREADS;
   const int sb0 = min(th * per, a.s.B), sb1 = min(sb0 + per, a.s.B);
-  uint32_t mine = 0;
-  for (int b = sb0; b < sb1; ++b) mine += tree_seq<R>(a, b, reporter).length(a);
-  uint32_t incl = mine;
+  uint2 mine = {0, 0};                 // tiles, units
+  for (int b = sb0; b < sb1; ++b) {
+    const TreeSeq t = tree_seq<R>(a, b, reporter);
+    const uint32_t n = t.units(a);
+    mine.x += n * t.tiles;
+    mine.y += n;
+  }
+  uint2 incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += o;
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl.x, off);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl.y, off);
+    if (lane >= off) {
+      incl.x += x;
+      incl.y += y;
+    }
   }
   if (lane == 31) m.scan[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  uint32_t before = incl - mine, total = 0;
+  uint2 below = {incl.x - mine.x, incl.y - mine.y}, all = {0, 0};
+#pragma unroll
   for (int w = 0; w < F::THREADS / 32; ++w) {
-    if (w < warp) before += m.scan[w];
-    total += m.scan[w];
+    const uint2 n = m.scan[w];
+    if (w < warp) {
+      below.x += n.x;
+      below.y += n.y;
+    }
+    all.x += n.x;
+    all.y += n.y;
   }
-  const Line line(total, gridDim.x);
+  const Line line(all.x, all.y, gridDim.x);
   const int cta = blockIdx.x;
   const bool active = cta < (int)line.runs;
   const uint32_t w0 = active ? line.start(cta) : 0;
-  if (active && w0 >= before && w0 < before + mine) {
+  const uint32_t before = below.x + line.cost * below.y;
+  if (active && w0 >= before && w0 < before + mine.x + line.cost * mine.y) {
     uint32_t at = before;
     for (int b = sb0; b < sb1; ++b) {
-      const uint32_t n = tree_seq<R>(a, b, false).length(a);
+      const TreeSeq t = tree_seq<R>(a, b, false);
+      const uint32_t n = t.units(a) * (t.tiles + line.cost);
       if (w0 < at + n) {
         m.start_b = b;
         m.start_off = w0 - at;
@@ -490,11 +510,11 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     // In the order in which the places come free: exponents and K of a tile,
     // then V of the tile before it.
     Cursor<R> cu;
-    cu.start(a, m.start_b, m.start_off, w0, line.start(cta + 1) - w0);
+    cu.start(a, line, m.start_b, m.start_off, w0, line.start(cta + 1) - w0);
     uint32_t jk = 0, jv = 0, g = 0, un = 0, nq = 0;
     int64_t row[2] = {-1, -1};         // of the tile, per MMA tile: this lane's page
     bool dead = false;
-    const int page = a.c.page;
+    const int page = a.c.page, page_bits = 31 - __clz(page);
     auto load_k = [&]() -> bool {
 #pragma unroll
       for (int h = 0; h < 2; ++h, ++jk) {
@@ -618,17 +638,30 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     Unit u;
     while (!dead && cu.next(a, line, cta, &u)) {
       for (int tile = u.first; tile < u.stop; ++tile) {
+        // this lane's page of either MMA tile; its number is on the way while a
+        // new unit is announced
+        unsigned first[2];
+        int pg[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          first[h] = (unsigned)tile * TILE + h * SUB + (unsigned)(lane * page);
+          pg[h] = -1;
+          if (lane * page < SUB && first[h] < u.end)
+            pg[h] = a.s.table[(int64_t)u.b * a.s.max_pages + (first[h] >> page_bits)];
+        }
+        if (tile == u.first && !announce(u, true)) {
+          dead = true;
+          break;
+        }
         int64_t now[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const unsigned t = (unsigned)tile * TILE + h * SUB + (unsigned)(lane * page);
           now[h] = -1;
-          if (lane * page < SUB && t < u.end) {
-            now[h] = row_of(a.c, a.s, u.b, t);
-            if (now[h] < 0)
-              atomicOr(a.err, kErrIndex);
+          if (lane * page < SUB && first[h] < u.end) {
+            if ((unsigned)pg[h] < (unsigned)a.c.pages)
+              now[h] = ((int64_t)pg[h] * a.c.Hkv + u.hk) * page;
             else
-              now[h] += (int64_t)u.hk * page;
+              atomicOr(a.err, kErrIndex);
           }
         }
         const int64_t was[2] = {row[0], row[1]};
@@ -642,11 +675,6 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         }
         load_e();
         if (!load_k()) {
-          dead = true;
-          break;
-        }
-        // (the unit's first copies are on their way before it is announced)
-        if (tile == u.first && !announce(u, true)) {
           dead = true;
           break;
         }
@@ -942,7 +970,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         }
         if (tree) {
           // the largest V exponent among what a row sees: one per row here
-#pragma unroll 1
+#pragma unroll 4
           for (int c = 0; c < C; ++c) {
             const uint32_t w = __reduce_max_sync(
                 0xffffffffu, max((vis[0] >> c) & 1 ? ve[0] : 0u, (vis[1] >> c) & 1 ? ve[1] : 0u));
@@ -1061,18 +1089,19 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) vr[i] = make_uint4(0, 0, 0, 0);
             } else if (t >= pos) {
-              bool any = false;
-#pragma unroll 1
+              uint32_t any = 0;        // a byte 0x7F without its sign carries into bit 7
+#pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 const uint4 x = vr[i];
-                const uint32_t n[4] = {__vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
-                                       __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
-                                       __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
-                                       __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)};
-                if (n[0] | n[1] | n[2] | n[3]) {
-                  any = true;
-                  vr[i] = make_uint4(x.x & ~n[0], x.y & ~n[1], x.z & ~n[2], x.w & ~n[3]);
-                }
+                any |= ((x.x & 0x7F7F7F7Fu) + 0x01010101u) | ((x.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                       ((x.z & 0x7F7F7F7Fu) + 0x01010101u) | ((x.w & 0x7F7F7F7Fu) + 0x01010101u);
+              }
+              any &= 0x80808080u;
+              if (any) {
+                uint32_t* vw = reinterpret_cast<uint32_t*>(vr);
+#pragma unroll 1
+                for (int i = 0; i < D / 4; ++i)
+                  vw[i] &= ~__vcmpeq4(vw[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
               }
               if (any) atomicOr(&m.nan_nodes, 1ull << (t - pos));
             }
@@ -1163,36 +1192,40 @@ __global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a
   using namespace ta;
   constexpr int V = D / 32, U = 8;
   __shared__ float part_o[8][D], part_l[8], part_m[8];
-  __shared__ uint32_t scan[8];
+  __shared__ uint32_t scan[8][4];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int unit = blockIdx.x;
   const int rb = unit % a.blocks, hk = unit / a.blocks % a.c.Hkv, b = unit / a.blocks / a.c.Hkv;
   const TreeSeq t = tree_seq<R>(a, b, false);
   Head hd = {0, 0};
   if (WPR > 1) {
-    // places below sequence b, and of all sequences
-    uint32_t below = 0, all = 0;
+    // tiles and units below sequence b, and of all sequences
+    uint32_t n[4] = {0, 0, 0, 0};
     for (int i = threadIdx.x; i < a.s.B; i += 256) {
-      const uint32_t n = tree_seq<R>(a, i, false).length(a);
-      all += n;
-      if (i < b) below += n;
+      const TreeSeq x = tree_seq<R>(a, i, false);
+      const uint32_t units = x.units(a), tiles = units * x.tiles;
+      n[0] += tiles;
+      n[1] += units;
+      if (i < b) {
+        n[2] += tiles;
+        n[3] += units;
+      }
     }
-    all = __reduce_add_sync(0xffffffffu, all);
-    below = __reduce_add_sync(0xffffffffu, below);
-    if (lane == 0) {
-      scan[warp] = all;
-      part_l[warp] = __uint_as_float(below);
-    }
-    __syncthreads();
-    all = below = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      all += scan[w];
-      below += __float_as_uint(part_l[w]);
+    for (int k = 0; k < 4; ++k) {
+      n[k] = __reduce_add_sync(0xffffffffu, n[k]);
+      if (lane == 0) scan[warp][k] = n[k];
     }
     __syncthreads();
-    const Line line(all, ctas);
-    const uint32_t at = below + (uint32_t)(hk * t.blocks + rb) * (t.tiles + UNIT_COST) + UNIT_COST;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      n[k] = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) n[k] += scan[w][k];
+    }
+    const Line line(n[0], n[1], ctas);
+    const uint32_t at = n[2] + line.cost * n[3] +
+                        (uint32_t)(hk * t.blocks + rb) * (t.tiles + line.cost) + line.cost;
     if (rb < t.blocks) {
       hd.run = (int)line.run_of(at);
       hd.follow = (int)line.run_of(at + t.tiles - 1) - hd.run;
