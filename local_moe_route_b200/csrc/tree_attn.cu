@@ -278,6 +278,18 @@ __device__ __forceinline__ void tmem_load2(uint32_t at0, uint32_t at1, uint32_t 
   }
 }
 
+// mbar_wait_warp with its slow path out of line: the waits are many and the
+// code between them runs from the instruction cache.
+__device__ __noinline__ bool ta_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          unsigned* err) {
+  return mbar_wait_warp(bar, parity, abort, err);
+}
+__device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                        unsigned* err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity))) return true;
+  return ta_wait_slow(bar, parity, abort, err);
+}
+
 // Pairs of fp32 values, one instruction for both.
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pair(uint32_t x, uint32_t y) {
@@ -521,7 +533,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         const int ks = jk % KS;
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, row[h] >= 0));
         if (jk >= (uint32_t)KS &&
-            !mbar_wait_warp(&m.k_empty[ks], (jk / KS - 1) & 1, abort_flag, a.err))
+            !ta_wait(&m.k_empty[ks], (jk / KS - 1) & 1, abort_flag, a.err))
           return false;
         if (lane == 0) mbar_arrive_expect_tx(&m.k_full[ks], n * page * D);
         __syncwarp();
@@ -537,7 +549,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         const int vs = jv % VS;
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, row[h] >= 0));
         if (jv >= (uint32_t)VS &&
-            !mbar_wait_warp(&m.v_empty[vs], (jv / VS - 1) & 1, abort_flag, a.err))
+            !ta_wait(&m.v_empty[vs], (jv / VS - 1) & 1, abort_flag, a.err))
           return false;
         if (lane == 0) mbar_arrive_expect_tx(&m.v_full[vs], n * page * D);
         __syncwarp();
@@ -579,7 +591,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     auto announce = [&](const Unit& u, bool some) -> bool {
       const int us = un % UNITS;
       if (un >= (uint32_t)UNITS &&
-          !mbar_wait_warp(&m.u_empty[us], (un / UNITS - 1) & 1, abort_flag, a.err))
+          !ta_wait(&m.u_empty[us], (un / UNITS - 1) & 1, abort_flag, a.err))
         return false;
       if (some) {
         const bool drafts = (unsigned)u.stop * TILE > (unsigned)u.pos;
@@ -604,7 +616,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
           up[j] = i < u.count ? i - 1 : -1;
           if (drafts && a.parent && i < u.count) up[j] = a.parent[(int64_t)u.b * a.s.N + i];
         }
-        if (un > 0 && !mbar_wait_warp(&m.qr_empty, (un - 1) & 1, abort_flag, a.err)) return false;
+        if (un > 0 && !ta_wait(&m.qr_empty, (un - 1) & 1, abort_flag, a.err)) return false;
         if (lane == 0) mbar_arrive_expect_tx(&m.qr_full, n * D * 2);
         __syncwarp();
         ++nq;
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         row[1] = now[1];
         // the exponents' slot is free once the first K place is
         if (jk >= (uint32_t)KS &&
-            !mbar_wait_warp(&m.k_empty[jk % KS], (jk / KS - 1) & 1, abort_flag, a.err)) {
+            !ta_wait(&m.k_empty[jk % KS], (jk / KS - 1) & 1, abort_flag, a.err)) {
           dead = true;
           break;
         }
@@ -708,7 +720,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       for (int h = 0; h < 2; ++h) {
         const uint32_t j = 2 * i + h;
         const int ks = j % KS;
-        if (!mbar_wait_warp(&m.k_full[ks], (j / KS) & 1, abort_flag, a.err)) return false;
+        if (!ta_wait(&m.k_full[ks], (j / KS) & 1, abort_flag, a.err)) return false;
         tc_fence_after();
         if (leader) {
 #pragma unroll
@@ -727,7 +739,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       for (int h = 0; h < 2; ++h) {
         const uint32_t j = 2 * i + h;
         const int vs = j % VS;
-        if (!mbar_wait_warp(&m.v_full[vs], (j / VS) & 1, abort_flag, a.err)) return false;
+        if (!ta_wait(&m.v_full[vs], (j / VS) & 1, abort_flag, a.err)) return false;
         tc_fence_after();
         if (leader) {
 #pragma unroll
@@ -747,19 +759,19 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
     bool dead = false;
     for (uint32_t un = 0; !dead; ++un) {
       const int us = un % UNITS;
-      if (!mbar_wait_warp(&m.u_full[us], (un / UNITS) & 1, abort_flag, a.err)) break;
+      if (!ta_wait(&m.u_full[us], (un / UNITS) & 1, abort_flag, a.err)) break;
       const int tiles = m.unit[us].stop - m.unit[us].first;
       const bool last = m.unit[us].last;
       __syncwarp();
       if (lane == 0) mbar_arrive(&m.u_empty[us]);
       if (last) break;
-      if (!mbar_wait_warp(&m.q_full, un & 1, abort_flag, a.err)) break;
+      if (!ta_wait(&m.q_full, un & 1, abort_flag, a.err)) break;
       tc_fence_after();
       if (!scores(g)) break;
       for (int i = 0; i < tiles; ++i, ++g) {
         // the next scores as soon as these have left TMEM
         if (i + 1 < tiles) {
-          if (!mbar_wait_warp(&m.s_free, g & 1, abort_flag, a.err)) {
+          if (!ta_wait(&m.s_free, g & 1, abort_flag, a.err)) {
             dead = true;
             break;
           }
@@ -769,7 +781,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
             break;
           }
         }
-        if (!mbar_wait_warp(&m.p_ready, g & 1, abort_flag, a.err)) {
+        if (!ta_wait(&m.p_ready, g & 1, abort_flag, a.err)) {
           dead = true;
           break;
         }
@@ -795,7 +807,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
 
     // O of tile i (sum of its high and low columns) into acc
     auto add_o = [&](uint32_t i) {
-      ok = mbar_wait_warp(&m.o_full, i & 1, abort_flag, a.err) && ok;
+      ok = ta_wait(&m.o_full, i & 1, abort_flag, a.err) && ok;
       tc_fence_after();
       const float* bo = m.beta_o[wg][i & 1];
       uint32_t hi[C], lo[C];
@@ -847,14 +859,14 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       // ---- a unit begins: its query rows, split and scaled, and what they see
       const int us = un % UNITS;
       const Unit& u = m.unit[us];
-      dead = !mbar_wait_warp(&m.u_full[us], (un / UNITS) & 1, abort_flag, a.err);
+      dead = !ta_wait(&m.u_full[us], (un / UNITS) & 1, abort_flag, a.err);
       if (named_barrier_or(1, ALL, dead)) break;
       if (u.last) break;
       const unsigned pos = (unsigned)u.pos;
       const bool drafts = (unsigned)u.stop * TILE > pos;     // the run reaches the tree
       if (th < NODES) m.seen_by[th][0] = m.seen_by[th][1] = 0;
       if (th == 0) m.nan_nodes = 0;
-      ok = mbar_wait_warp(&m.qr_full, un & 1, abort_flag, a.err) && ok;
+      ok = ta_wait(&m.qr_full, un & 1, abort_flag, a.err) && ok;
       constexpr int LPR = D / 8;             // lanes per row, 8 values each
 #pragma unroll 1
       for (int r0 = 0; r0 < R; r0 += ALL / LPR) {
@@ -910,7 +922,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       const int first_tile = u.first, stop = dead ? u.first : u.stop;
       const unsigned end = u.end;
       for (int tile = first_tile; tile < stop; ++tile, ++g) {
-        ok = mbar_wait_warp(&m.e_full[g % ES], (g / ES) & 1, abort_flag, a.err) && ok;
+        ok = ta_wait(&m.e_full[g % ES], (g / ES) & 1, abort_flag, a.err) && ok;
         const uint8_t* e = sE + (g % ES) * 2 * TILE + lt;
         const uint32_t ke[2] = {e[0], e[SUB]}, ve[2] = {e[TILE], e[TILE + SUB]};
         const bool tree = (unsigned)(tile + 1) * TILE > pos;  // nodes, or the end
@@ -928,7 +940,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
               vis[h] = m.seen_by[t - pos][wg * C / 32] >> (wg * C % 32);
           }
         }
-        ok = mbar_wait_warp(&m.s_full, g & 1, abort_flag, a.err) && ok;
+        ok = ta_wait(&m.s_full, g & 1, abort_flag, a.err) && ok;
         tc_fence_after();
         float s[2][C];
 #pragma unroll
@@ -1082,7 +1094,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const uint32_t j = 2 * g + h;
-            ok = mbar_wait_warp(&m.v_full[j % VS], (j / VS) & 1, abort_flag, a.err) && ok;
+            ok = ta_wait(&m.v_full[j % VS], (j / VS) & 1, abort_flag, a.err) && ok;
             const unsigned t = (unsigned)tile * TILE + h * SUB + lt;
             uint4* vr = reinterpret_cast<uint4*>(sV + (j % VS) * F::KV_BYTES + lt * D);
             if (t >= end || e[h * SUB] == 0 || e[TILE + h * SUB] == 0) {
