@@ -61,15 +61,11 @@ __host__ __device__ constexpr uint32_t unit_cost(uint32_t tiles, uint32_t ctas) 
   return tiles >= 16 * ctas ? 3 : tiles >= 4 * ctas ? 2 : tiles > ctas ? 1 : 0;
 }
 constexpr int UNITS = 4;                    // units announced ahead
-#ifndef TA_C16
-#define TA_C16 16
-#endif
-constexpr int C16 = TA_C16;
+constexpr int C = 16;                       // row columns per softmax warpgroup
 
 template <int D, int R>
 struct Cfg {
-  static constexpr int C = R == 16 ? C16 : 16;         // row columns per softmax warpgroup
-  static constexpr int NWG = R / C;
+  static constexpr int NWG = R / C;                    // softmax warpgroups
   static constexpr int CTAS = R == 64 ? 1 : 2;         // per SM
   // K and V rings, in MMA tiles
   static constexpr int KS = (R == 64 ? 4 : 2) * (D == 64 ? 2 : 1);
@@ -116,13 +112,13 @@ struct Misc {
   int start_b;
   int nan_row[R];
   alignas(16) float qf[R];                       // score factor of the row
-  alignas(16) float wmax[F::NWG][4][F::C];       // per warp: largest score of the tile
-  alignas(16) uint32_t wexp[F::NWG][4][F::C];    // per warp: largest visible V exponent
+  alignas(16) float wmax[F::NWG][4][C];       // per warp: largest score of the tile
+  alignas(16) uint32_t wexp[F::NWG][4][C];    // per warp: largest visible V exponent
   uint32_t wtop[F::NWG][4];
-  alignas(16) float mref[F::NWG][F::C], beta[F::NWG][F::C], alpha[F::NWG][F::C];
-  alignas(16) float beta_o[F::NWG][2][F::C];
-  alignas(16) float eh[F::NWG][F::C];            // a row's V exponent as a factor
-  alignas(16) float lsum[F::NWG][4][F::C];       // per warp: sums of the weights
+  alignas(16) float mref[F::NWG][C], beta[F::NWG][C], alpha[F::NWG][C];
+  alignas(16) float beta_o[F::NWG][2][C];
+  alignas(16) float eh[F::NWG][C];            // a row's V exponent as a factor
+  alignas(16) float lsum[F::NWG][4][C];       // per warp: sums of the weights
   alignas(16) float inv[R];                      // 1 / (sum * WSCALE)
 };
 
@@ -260,22 +256,13 @@ struct Cursor {
   }
 };
 
-// 32 lanes x N consecutive columns, waited for.
-template <int N>
-__device__ __forceinline__ void tmem_load2(uint32_t at0, uint32_t at1, uint32_t (&x)[N],
-                                           uint32_t (&y)[N]) {
-  if constexpr (N == 16) {
-    tmem_ld_32x32b_x16(at0, x);
-    tmem_ld_32x32b_x16(at1, y);
-    tmem_ld_wait_regs(x);
-    tmem_ld_wait_regs(y);
-  } else {
-    static_assert(N == 8, "columns per warpgroup");
-    tmem_ld_32x32b_x8(at0, x);
-    tmem_ld_32x32b_x8(at1, y);
-    tmem_ld_wait_regs(x);
-    tmem_ld_wait_regs(y);
-  }
+// 32 lanes x 16 consecutive columns from either address, waited for.
+__device__ __forceinline__ void tmem_load2(uint32_t at0, uint32_t at1, uint32_t (&x)[16],
+                                           uint32_t (&y)[16]) {
+  tmem_ld_32x32b_x16(at0, x);
+  tmem_ld_32x32b_x16(at1, y);
+  tmem_ld_wait_regs(x);
+  tmem_ld_wait_regs(y);
 }
 
 // mbar_wait_warp with its slow path out of line: the waits are many and the
@@ -414,7 +401,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
                      const __grid_constant__ CUtensorMap map_v, const TreeArgs a) {
   using namespace ta;
   using F = Cfg<D, R>;
-  constexpr int NWG = F::NWG, C = F::C, KS = F::KS, VS = F::VS, ES = F::ES;
+  constexpr int NWG = F::NWG, KS = F::KS, VS = F::VS, ES = F::ES;
   using M = Misc<F, R>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sK = smem + F::K_OFF;
@@ -811,7 +798,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       tc_fence_after();
       const float* bo = m.beta_o[wg][i & 1];
       uint32_t hi[C], lo[C];
-      tmem_load2<C>(lanes_at + F::O_COL, lanes_at + F::O_COL + R, hi, lo);
+      tmem_load2(lanes_at + F::O_COL, lanes_at + F::O_COL + R, hi, lo);
 #pragma unroll
       for (int c = 0; c < C; c += 4) {
         const float4 b4 = *reinterpret_cast<const float4*>(bo + c);
@@ -947,7 +934,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         for (int h = 0; h < 2; ++h) {
           const f32x2 kf = pair(ke[h] << 23, ke[h] << 23);
           uint32_t hi[C], lo[C];
-          tmem_load2<C>(lanes_at + h * 2 * R, lanes_at + h * 2 * R + R, hi, lo);
+          tmem_load2(lanes_at + h * 2 * R, lanes_at + h * 2 * R + R, hi, lo);
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
             const float4 f4 = *reinterpret_cast<const float4*>(&m.qf[wg * C + c]);
@@ -1127,13 +1114,8 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
           for (int i = 0; i < C / 4; ++i) split4(ph[h][2 * i], ph[h][2 * i + 1], &hi[i], &lo[i]);
           uint8_t* to_hi = sP + sw_off<2 * R>(h * SUB + lt, wg * C);
           uint8_t* to_lo = sP + sw_off<2 * R>(h * SUB + lt, R + wg * C);
-          if constexpr (C == 16) {
-            *reinterpret_cast<uint4*>(to_hi) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(to_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          } else {
-            *reinterpret_cast<uint2*>(to_hi) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(to_lo) = make_uint2(lo[0], lo[1]);
-          }
+          *reinterpret_cast<uint4*>(to_hi) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         // also orders this thread's reads of the exponents before a later copy there
         fence_proxy_async_smem();
