@@ -112,9 +112,10 @@ STRATA_API strata_status_t strata_kv_read(strata_kv_cache_t cache, strata_kv_seq
  *   out      [B][N][Hq][D] bf16; rows of slots behind count[b] are left as they
  *            were; a node that sees no row gets zeros
  * Values at positions a node does not see, NaN among them, do not reach it.
- * Scores, softmax and sums in fp32; the weights of a tile of 128 positions are
- * rounded to 2^-9 of their value (and 2^-18 of the tile's largest weight times
- * the scale of its largest V row) for the product with V.
+ * Scores, softmax and sums in fp32; for the product with V the weights of a tile
+ * of 256 positions are rounded to 2^-9 of their value, or to 2^-17.8 of the
+ * tile's largest weight (times the V scale of the row it belongs to, if that is
+ * the smaller one) where that is more.
  *   ws       scratch of strata_tree_attention_workspace_bytes() bytes, which
  *            reads the sizes of `cache` and `seqs` only (0 = refused) */
 STRATA_API size_t strata_tree_attention_workspace_bytes(strata_kv_cache_t cache,
@@ -128,7 +129,9 @@ STRATA_API strata_status_t strata_tree_attention(strata_kv_cache_t cache, strata
  * numbers: the tokens that come out are distributed as if drawn from the
  * target one by one.
  *   B sequences, N nodes (1 .. STRATA_TREE_MAX_NODES), V tokens in the vocabulary;
- *   B * N < 2^24, V < 2^30 */
+ *   B * N < 2^24, V <= STRATA_VERIFY_MAX_VOCAB (a sequence's sums of four
+ *   probabilities stay in shared memory) */
+#define STRATA_VERIFY_MAX_VOCAB 800000
 typedef struct {
   int32_t B, N, V;
 } strata_verify_dims_t;

@@ -127,7 +127,7 @@ strata_status_t strata_verify_drafts(const int32_t* tokens, const int32_t* paren
                                      int32_t* out_tokens, strata_stream_t stream) {
   if (dims.B < 0 || dims.N <= 0 || dims.V <= 0) return STRATA_ERR_INVALID_ARG;
   if (dims.N > STRATA_TREE_MAX_NODES || (int64_t)dims.B * dims.N >= (1 << 24) ||
-      dims.V >= (1 << 30))
+      dims.V > STRATA_VERIFY_MAX_VOCAB)
     return STRATA_ERR_UNSUPPORTED;
   if (dims.B == 0) return STRATA_OK;
   if (!ok_ptr(tokens) || !ok_opt(parent) || !ok_opt(count) || !ok_ptr(p) || !ok_opt(q) ||

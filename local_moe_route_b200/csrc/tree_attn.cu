@@ -32,14 +32,35 @@
 // below an earlier tile's maximum keep their precision.  References are
 // integers (log2 domain), so rescaling is an exponent addition.
 //
-// Work: the tiles of all (sequence, KV head, block of R rows) units in one
-// line, cut into equal runs, one per CTA, whatever the lengths are.  A unit
-// that lies in one run is finished there; the others leave partial sums
-// that tree_attn_combine_kernel joins in run order.
+// Work: the tiles (256 positions) of all (sequence, KV head, block of R rows)
+// units in one line, cut into equal runs, one per CTA, whatever the lengths are.
+// A unit that lies in one run is finished there; the others leave partial sums
+// that tree_attn_combine_kernel joins in run order (no atomics, so results do
+// not depend on the order in which CTAs run).
 //
-// Roles per CTA: a warp that issues the TMA copies of pages (K, V, exponents)
-// into a ring of tiles, a warp that issues the MMAs, and one warpgroup per 32
-// row columns (16 when R = 16) for the softmax, the weights and the running sums.
+// Roles per CTA: a warp that follows the run, announces its units and issues
+// the TMA copies of pages (K, V, exponents, query rows) into rings of tiles, a
+// warp that issues the MMAs, and one warpgroup per 16 row columns for the
+// softmax, the weights and the running sums.  K and V places come free at
+// different times (after the scores, after the output), so they are separate
+// rings; the next tile's scores are issued as soon as these have left TMEM.
+//
+// R, the rows per block, is 16, 32 or 64: the smallest that holds all rows of
+// N nodes, 64 at most (the instruction's width is 2R = 128, and the sums of 64 rows
+// need 4 warpgroups' registers).  Two CTAs per SM at R <= 32, one at 64 (TMEM).
+//
+// Measured (D = 128, 4 KV heads, 32 query heads, one call, burst clocks): 32
+// sequences of 4 nodes behind up to 34,000 positions 108 us, 5.4 TB/s of the
+// cache's bytes (0.82 of the copy rate; the same with one node 97 us); one
+// sequence behind 34,000 22 us; one token behind 300 positions 11 us, of which 2 us
+// are the launch, 6 us the first tile's chain of dependent steps (lengths -> page
+// -> copy -> scores) and 2 us the join.  In a long line a tile takes a CTA
+// 3.3 us, with two CTAs per SM near what its 66 KB take at the copy rate; D = 64
+// halves the bytes but not the arithmetic (100 us): the softmax warps then issue
+// about half of the time and wait for each other the rest.  Steps that did not
+// help: the last fifth of the line in small runs taken from a counter (141 us
+// against 126: a run costs two tiles), one barrier per tile with every warp
+// working out the references (112 against 108), 8 columns per warpgroup.
 #include <cuda_fp8.h>
 
 #include "common.cuh"

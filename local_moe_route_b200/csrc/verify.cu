@@ -12,8 +12,17 @@
 //
 // One cluster of 8 CTAs per sequence shares the vocabulary: each warp
 // of the cluster owns one contiguous run of it, sums it, and the sums meet in
-// rank 0's .. 7's shared memory in a fixed order.  The same per-warp sums find
-// the warp whose run holds the next token, and only that run is read again.
+// rank 0's .. 7's shared memory in a fixed order.  On the pass for the next
+// token the sums of every four values stay in shared memory, so finding it
+// takes one more load.
+//
+// Bound by the chain of passes of the sequence with the most rejections: a
+// pass over 100,003 tokens of p and q takes about 4.2 us (2.7 us the sums, of which
+// 0.8 us are the conversions to 64 bits, 0.9 us the cluster's barrier); a greedy
+// chain of 3 drafts at 32,000 tokens takes 6.3 us in all, 32 trees of 16 nodes at
+// 100,003 tokens 27 us.  Holding a node's rows in shared memory between its
+// passes was no faster (29.7 against 31.4 us then, and slower without
+// rejections), nor were 256 or 1024 threads.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -71,13 +80,14 @@ struct RestRow {
       }
     }
   }
+  template <bool Q>
   __device__ __forceinline__ void values(int blk, const float (&pv)[4], const float (&qv)[4],
                                          double (&r)[4]) const {
     const int x0 = 4 * blk - shift;
 #pragma unroll
     for (int j = 0; j < 4; ++j)      // (elements outside the row were loaded as 0)
-      r[j] = q ? rest(pv[j], qv[j]) : (double)pv[j];
-    if (!q)
+      r[j] = Q ? rest(pv[j], qv[j]) : (double)pv[j];
+    if (!Q)
       for (int i = 0; i < n_gone; ++i) {
         const int d = gone[i] - x0;
 #pragma unroll
@@ -93,14 +103,13 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// Sum of blocks [b0, b1) by one warp, the same in every lane.
+// Sum of blocks [b0, b1) by one warp, the same in every lane.  `keep`, when
+// given, gets the blocks' own sums.
 template <bool Q>
-__device__ __forceinline__ double run_sum(const RestRow& row, int b0, int b1, int lane) {
-  constexpr int U = 2;
-  double s0 = 0.0, s1 = 0.0;
-  auto add = [](double& s, double r) {
-    if (r > 0.0) s += r;
-  };
+__device__ __forceinline__ double run_sum(const RestRow& row, int b0, int b1, int lane,
+                                          double* keep) {
+  constexpr int U = 2;     // 3, 4 and 8 were no faster: the rows come from L2 or once
+  double sum = 0.0;
   for (int blk = b0 + lane; blk < b1; blk += 32 * U) {
     float pv[U][4], qv[U][4];
 #pragma unroll
@@ -111,21 +120,14 @@ __device__ __forceinline__ double run_sum(const RestRow& row, int b0, int b1, in
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (Q) {
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          add(s0, fma(-row.c, (double)qv[u][j], (double)pv[u][j]));
-          add(s1, fma(-row.c, (double)qv[u][j + 1], (double)pv[u][j + 1]));
-        }
-      } else {
-        double r[4];
-        row.values(blk + 32 * u, pv[u], qv[u], r);
-        s0 += r[0] + r[1];
-        s1 += r[2] + r[3];
-      }
+      double r[4];
+      row.values<Q>(blk + 32 * u, pv[u], qv[u], r);
+      const double s = (r[0] + r[1]) + (r[2] + r[3]);
+      sum += s;
+      if (keep && blk + 32 * u < b1) keep[blk + 32 * u - b0] = s;
     }
   }
-  return warp_sum(s0 + s1);
+  return warp_sum(sum);
 }
 
 __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREADS, 2)
@@ -136,6 +138,7 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
                   int32_t* __restrict__ path_len, int32_t* __restrict__ out_tokens,
                   unsigned* err) {
   using namespace vd;
+  extern __shared__ double block_sums[];     // of this CTA's blocks, for the next token
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int b = blockIdx.x / CLUSTER;
@@ -189,13 +192,14 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
   int turn = 0;
   // The sum of r over the row, equal in every thread of the cluster; leaves the
   // warps' sums in sums[turn].
-  auto total = [&](const RestRow& row) -> double {
+  auto total = [&](const RestRow& row, bool keep) -> double {
     turn ^= 1;
     const int blocks = (row.shift + V + 3) / 4;
     const int per = (blocks + CLUSTER * WARPS - 1) / (CLUSTER * WARPS);
     const int w = rank * WARPS + warp;
     const int b0 = min(w * per, blocks), b1 = min(b0 + per, blocks);
-    const double s = row.q ? run_sum<true>(row, b0, b1, lane) : run_sum<false>(row, b0, b1, lane);
+    double* at = keep ? block_sums + warp * per : nullptr;
+    const double s = row.q ? run_sum<true>(row, b0, b1, lane, at) : run_sum<false>(row, b0, b1, lane, at);
     if (lane < CLUSTER) cluster.map_shared_rank(&sums[turn][0], lane)[w] = s;
     cluster.sync();
     double t = 0.0;
@@ -224,7 +228,7 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
     if (par_s[i] != cur) continue;
     const int x = tok_s[i];
     if ((unsigned)x >= (unsigned)V) continue;
-    if (!known) S = total(row_at());
+    if (!known) S = total(row_at(), false);
     known = true;
     if ((double)u_s[i] * (double)q_s[i] * S < row_at().one(p_s[i], q_s[i], x)) {
       cur = i;
@@ -245,7 +249,7 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
   // the next token
   const RestRow row = row_at();
   __syncthreads();
-  const double sum = total(row);
+  const double sum = total(row, true);
   const double want = (double)u_sample[b] * sum;
   // the run that holds it: the first whose running sum exceeds `want`, else
   // the last with a positive sum.  Every warp scans the sums, four to a lane.
@@ -290,53 +294,58 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
     const int blocks = (row.shift + V + 3) / 4;
     const int per = (blocks + CLUSTER * WARPS - 1) / (CLUSTER * WARPS);
     const int b0 = min(run * per, blocks), b1 = min(b0 + per, blocks);
-    // each lane takes a contiguous share, U blocks of it at a time
-    constexpr int U = 4;
-    int found = -1, fallback = -1;
-    double base = below_run;
-    for (int k0 = b0; k0 < b1 && found < 0; k0 += 32 * U) {
-      const int share = min(U, (b1 - k0 + 31) / 32);
-      const int l0 = k0 + lane * share;
-      float pv[U][4], qv[U][4];
+    // the block: each lane takes a contiguous share of the run's sums
+    const double* sum_of = block_sums + warp * per;
+    const int share = (b1 - b0 + 31) / 32;
+    const int l0 = min(lane * share, b1 - b0), l1 = min(l0 + share, b1 - b0);
+    double mine_sum = 0.0;
+    for (int i = l0; i < l1; ++i) mine_sum += sum_of[i];
+    double to = mine_sum;                        // sum of lanes 0 .. lane
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < share && l0 + u < b1) row.load(l0 + u, pv[u], qv[u]);
-      double mine_sum = 0.0;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < share && l0 + u < b1) {
-          double r[4];
-          row.values(l0 + u, pv[u], qv[u], r);
-          mine_sum += (r[0] + r[1]) + (r[2] + r[3]);
+    for (int off = 1; off < 32; off <<= 1) {
+      const double o = __shfl_up_sync(0xffffffffu, to, off);
+      if (lane >= off) to += o;
+    }
+    double run_at = __shfl_up_sync(0xffffffffu, to, 1);
+    run_at = below_run + (lane ? run_at : 0.0);
+    int blk_hit = -1, blk_pos = -1;
+    double hit_from = 0.0, pos_from = 0.0;
+    for (int i = l0; i < l1; ++i) {
+      const double s = sum_of[i];
+      if (s > 0.0) {
+        blk_pos = i;
+        pos_from = run_at;
+        if (blk_hit < 0 && run_at + s > want) {
+          blk_hit = i;
+          hit_from = run_at;
         }
-      double to = mine_sum;                      // sum of lanes 0 .. lane
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, to, off);
-        if (lane >= off) to += o;
       }
-      const double before = __shfl_up_sync(0xffffffffu, to, 1);
-      double run_at = base + (lane ? before : 0.0);
-      int x_hit = -1, x_pos = -1;
+      run_at += s;
+    }
+    const unsigned b_hits = __ballot_sync(0xffffffffu, blk_hit >= 0);
+    const unsigned b_some = __ballot_sync(0xffffffffu, blk_pos >= 0);
+    const int src = b_hits ? __ffs(b_hits) - 1 : b_some ? 31 - __clz(b_some) : 0;
+    const int in = __shfl_sync(0xffffffffu, b_hits ? blk_hit : blk_pos, src);
+    run_at = __shfl_sync(0xffffffffu, b_hits ? hit_from : pos_from, src);
+    // the token in it
+    int found = -1, fallback = -1;
+    if (in >= 0) {
+      const int blk = b0 + in;
+      float pv[4] = {0.f, 0.f, 0.f, 0.f}, qv[4] = {0.f, 0.f, 0.f, 0.f};
+      row.load(blk, pv, qv);
+      double r[4];
+      if (row.q)
+        row.values<true>(blk, pv, qv, r);
+      else
+        row.values<false>(blk, pv, qv, r);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < share && l0 + u < b1) {
-          double r[4];
-          row.values(l0 + u, pv[u], qv[u], r);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            run_at += r[j];
-            if (r[j] > 0.0) {
-              x_pos = 4 * (l0 + u) - row.shift + j;
-              if (x_hit < 0 && run_at > want) x_hit = x_pos;
-            }
-          }
+      for (int j = 0; j < 4; ++j) {
+        run_at += r[j];
+        if (r[j] > 0.0) {
+          fallback = 4 * blk - row.shift + j;
+          if (found < 0 && run_at > want) found = fallback;
         }
-      const unsigned x_hits = __ballot_sync(0xffffffffu, x_hit >= 0);
-      const unsigned x_some = __ballot_sync(0xffffffffu, x_pos >= 0);
-      if (x_some) fallback = __shfl_sync(0xffffffffu, x_pos, 31 - __clz(x_some));
-      if (x_hits) found = __shfl_sync(0xffffffffu, x_hit, __ffs(x_hits) - 1);
-      base += __shfl_sync(0xffffffffu, to, 31);
+      }
     }
     if (found < 0) found = fallback < 0 ? 0 : fallback;
     for (int i = lane; i < N; i += 32) {
@@ -355,9 +364,15 @@ cudaError_t launch_verify(const int32_t* tokens, const int32_t* parent, const in
                           const float* u_sample, int B, int N, int V, int32_t* path,
                           int32_t* path_len, int32_t* out_tokens, unsigned* err,
                           cudaStream_t stream) {
-  verify_kernel<<<B * vd::CLUSTER, vd::THREADS, 0, stream>>>(tokens, parent, count, p, q, u_accept,
-                                                             u_sample, N, V, path, path_len,
-                                                             out_tokens, err);
+  const int per = ((V + 3) / 4 + 1 + vd::CLUSTER * vd::WARPS - 1) / (vd::CLUSTER * vd::WARPS);
+  const size_t bytes = (size_t)per * vd::WARPS * sizeof(double);
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+  }
+  verify_kernel<<<B * vd::CLUSTER, vd::THREADS, bytes, stream>>>(
+      tokens, parent, count, p, q, u_accept, u_sample, N, V, path, path_len, out_tokens, err);
   return cudaGetLastError();
 }
 

@@ -19,12 +19,13 @@ from typing import Any, Optional
 from . import STRATA_ERR_INVALID_ARG, StrataError, _nbytes, _stream, lib
 
 __all__ = [
-    "STRATA_TREE_MAX_NODES", "KvCache", "KvSeqs", "VerifyDims", "strata_kv_append",
-    "strata_kv_read", "strata_kv_commit", "strata_tree_attention",
+    "STRATA_TREE_MAX_NODES", "STRATA_VERIFY_MAX_VOCAB", "KvCache", "KvSeqs", "VerifyDims",
+    "strata_kv_append", "strata_kv_read", "strata_kv_commit", "strata_tree_attention",
     "strata_tree_attention_workspace_bytes", "tree_attention_workspace", "strata_verify_drafts",
 ]
 
 STRATA_TREE_MAX_NODES = 64
+STRATA_VERIFY_MAX_VOCAB = 800000
 
 
 class _Refused(Exception):

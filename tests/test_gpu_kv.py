@@ -9,8 +9,8 @@ range).  Attention, per value, with A = sum_j p_j |v_j| / sum p:
     2^-11, and their floor: a tile's largest weight is scaled to 224 .. 448,
     e4m3's smallest step is 2^-9, so a weight is off by 2^-10 / 224 = 2^-17.8 of the
     tile's largest at most, in units of the tile's largest V scale, whose codes
-    reach 448 where its row may hold 224: over 128 positions 2^-9.8 of the largest
-    |V| value;
+    reach 448 where its row may hold 224: over the 256 positions of a tile 256 *
+    2^-17.8 * 2 = 2^-8.8 of the largest |V| value;
   * the scores: q is split into two e4m3 values, exact down to 2^-17 of the
     row's largest, and D products are summed in fp32 (2^-24 each): an error ds of
     a score changes a weight by about ds, numerator and denominator each.
@@ -266,7 +266,7 @@ def attention_bound(a, parent, q, scale):
                 A = vs.max(0)[None, :]                       # at least sum p |v| / sum p
                 bound[b, :n, h] = (2.0 ** -8 * np.abs(np.nan_to_num(ref[b, :n, h]))
                                    + A * (2.0 ** -9 + 2.0 ** -11 + 2.5 * ds[:, None])
-                                   + 2.0 ** -9.8 * vs.max(initial=0.0))
+                                   + 2.0 ** -8.8 * vs.max(initial=0.0))
     return ref, bound
 
 
@@ -320,6 +320,12 @@ ATTEND = [  # pos, count, N, Hq, Hkv, D, page, kind
     ([33], None, 2, 5, 5, 128, 128, "chain"),
     ([1500, 20], None, 7, 7, 1, 64, 64, "tree"),
     ([4000, 10, 0], [16, 16, 2], 16, 16, 2, 128, 64, "tree"),
+    ([0, 300, 7], [0, 0, 0], 4, 8, 2, 128, 16, "chain"),                    # nothing to do
+    ([300, 40, 0, 511, 512, 513, 9, 70] * 12, [2, 0, 1, 2, 1, 0, 2, 1] * 12, 2, 3, 3, 64, 16,
+     "forest"),                                                             # 96 short sequences
+    ([2047, 2048, 255, 256, 257, 1], None, 1, 64, 4, 64, 128, "chain"),     # ends at tile edges
+    ([190], None, 64, 64, 1, 64, 32, "tree"),                               # 4096 rows
+    ([9000, 1], [1, 33], 33, 4, 4, 64, 16, "tree"),                         # one long, one short
 ]
 
 
@@ -501,3 +507,99 @@ def test_binding_refuses_other_types_shapes_and_layouts(dev):
     with pytest.raises(sm.StrataError):
         sm.KvCache.of(a.t["k"], a.t["v"][:1], a.t["k_exp"], a.t["v_exp"])
     assert_device_ok()
+
+
+def test_cache_of_more_than_four_gib(dev):
+    """Rows past 2^32 bytes of codes: appended, read, attended to and moved."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB of free device memory")
+    pages, page, Hkv, D = 40000, 128, 8, 128                       # 5.2 GB of K, and of V
+    c = sm.KvCache.empty(pages, page, Hkv, D, dev)
+    rng = np.random.default_rng(90)
+    table = np.array([[39999, 5, 39000], [33000, 39998, 7]], np.int32)
+    pos, N, Hq = np.array([0, 0], np.int32), 300, 8
+    s = sm.KvSeqs.of(up(table, dev), up(pos, dev), N=N)
+    k, v = (bf16_bits(rng.standard_normal((2, N, Hkv, D)).astype(np.float32)) for _ in "kv")
+    sm.check(sm.strata_kv_append(c, s, up_bf16(k, dev), up_bf16(v, dev)))
+    out = [torch.empty((2, N, Hkv, D), dtype=torch.bfloat16, device=dev) for _ in "kv"]
+    sm.check(sm.strata_kv_read(c, s, *out))
+    assert_device_ok()
+    # the same through a small cache
+    small = Setup(rng, dev, pos, None, N, Hkv, D, page)
+    osp.append(small.cache, small.table, pos, None, k, v)
+    ref = osp.read(small.cache, small.table, pos, None, N)
+    for o, r in zip(out, ref):
+        assert np.array_equal(bf16_to_f64(bf16_host(o)), r)
+    n = 8
+    at = np.array([N - n, N - n - 40], np.int32)
+    q = bf16_bits(rng.standard_normal((2, n, Hq, D)).astype(np.float32))
+    small.pos, small.N = at, n
+    small.count = None
+    small.upload(dev)
+    t = sm.KvSeqs.of(up(table, dev), up(at, dev), N=n)
+    big = torch.full((2, n, Hq, D), -7.0, dtype=torch.bfloat16, device=dev)
+    ws = sm.tree_attention_workspace(c, t, Hq, dev)
+    sm.check(sm.strata_tree_attention(c, t, None, up_bf16(q, dev), 0.0, big, ws))
+    assert_device_ok()
+    check_attention(small, None, q, big)
+    path = np.array([[0, 3, 4, 7, -1, -1, -1, -1], [0, 1, 2, 6, -1, -1, -1, -1]], np.int32)
+    new = torch.zeros(2, dtype=torch.int32, device=dev)
+    sm.check(sm.strata_kv_commit(c, t, up(path, dev), up(np.array([4, 4], np.int32), dev), new))
+    osp.commit(small.cache, small.table, at, path, np.array([4, 4]))
+    sm.check(sm.strata_kv_read(c, s, *out))
+    assert_device_ok()
+    for o, r in zip(out, osp.read(small.cache, small.table, pos, None, N)):
+        assert np.array_equal(bf16_to_f64(bf16_host(o)), r)
+    assert new.cpu().tolist() == (at + 4).tolist()
+
+
+def test_attention_with_a_huge_value_at_a_hidden_sibling(dev):
+    """A sibling's V far larger than all others takes nothing from the rows that
+    do not see it; a large committed value beside small ones keeps the bound."""
+    rng = np.random.default_rng(91)
+    a = Setup(rng, dev, [200], None, 6, 2, 128, 16)
+    parent = np.array([[-1, 0, 0, 1, 2, 3]], np.int32)
+    t = 201                                          # node 1: not seen by 0, 2 and 4
+    a.cache["v_exp"][a.table[0, t // 16], :, t % 16] = 127 + 90
+    a.upload(dev)
+    q = bf16_bits(rng.standard_normal((1, 6, 8, 128)).astype(np.float32))
+    out = run_attention(a, parent, q, dev)
+    assert_device_ok()
+    got = bf16_to_f64(bf16_host(out))
+    ref, bound = attention_bound(a, parent, q, None)
+    for i in (0, 2, 4):                              # the bound without the sibling's V
+        keep = a.cache["v_exp"].copy()
+        a.cache["v_exp"][a.table[0, t // 16], :, t % 16] = 119
+        _, fine = attention_bound(a, parent, q, None)
+        a.cache["v_exp"] = keep
+        assert np.all(np.abs(got[0, i] - ref[0, i]) <= fine[0, i])
+    assert np.all(np.abs(got - ref) <= bound)
+
+
+def test_attention_keeps_a_sink_and_a_long_tail_apart(dev):
+    """One position with almost all the weight and thousands of small equal ones: the
+    tail's share of the output (about a quarter) is not lost to the weights' floor."""
+    D, n = 64, 6000
+    c = sm.KvCache.empty(400, 16, 1, D, dev)
+    k = np.zeros((1, n, 1, D), np.float32)
+    v = np.zeros((1, n, 1, D), np.float32)
+    k[0, 0, 0, 0] = 1.0
+    v[0, 0, 0, 0] = 1.0
+    v[0, 1:, 0, 1] = 1.0
+    s = sm.KvSeqs.of(torch.arange(400, dtype=torch.int32, device=dev).view(1, 400),
+                     torch.zeros(1, dtype=torch.int32, device=dev), N=n)
+    sm.check(sm.strata_kv_append(c, s, up_bf16(bf16_bits(k), dev), up_bf16(bf16_bits(v), dev)))
+    t = sm.KvSeqs.of(s.tensors[0], torch.full((1,), n - 1, dtype=torch.int32, device=dev), N=1)
+    q = np.zeros((1, 1, 1, D), np.float32)
+    q[..., 0] = 1.0
+    out = torch.zeros((1, 1, 1, D), dtype=torch.bfloat16, device=dev)
+    ws = sm.tree_attention_workspace(c, t, 1, dev)
+    scale = float(np.log(3.0 * (n - 1)))             # the sink weighs three times the tail
+    sm.check(sm.strata_tree_attention(c, t, None, up_bf16(bf16_bits(q), dev), scale, out, ws))
+    assert_device_ok()
+    got = bf16_to_f64(bf16_host(out))[0, 0, 0]
+    # every weight is off by 2^-9 at most (a tail tile's own largest is the tail's
+    # weight; beside the sink 255 tail positions keep 2^-17.8 of it each), bf16 2^-8
+    off = 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -11 + 255 * 2.0 ** -17.8
+    assert abs(got[0] - 0.75) <= 0.75 * off and abs(got[1] - 0.25) <= 0.25 * (2.0 ** -8 + 2.0 ** -9
+                                                                          + 2.0 ** -11) + 255 * 2.0 ** -17.8

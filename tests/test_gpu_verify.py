@@ -91,6 +91,10 @@ def test_verify_sizes_counts_and_many_rejections(dev):
     check(b, run(b, dev))
     c = make(rng, 300, 3, 64, "chain")
     check(c, run(c, dev))
+    d = make(rng, 1, 3, sm.STRATA_VERIFY_MAX_VOCAB, "star")
+    check(d, run(d, dev))
+    d["q"] = None
+    check(d, run(d, dev))
 
 
 def test_verify_equal_rows_and_extreme_random_numbers(dev):
