@@ -32,42 +32,49 @@ class _Refused(Exception):
     """A tensor argument the entry point would misread."""
 
 
-_torch = None      # torch, imported with the first tensor that is checked
-
-
-def _load_torch():
-    global _torch
-    import torch
-    _torch = torch
-    return torch
-
-
-def _dev(t: Any, dtype: str, elements: Optional[int] = None) -> Optional[int]:
-    """Pointer of a dense tensor of the current device with the given type (and
-    number of elements); None and raw pointers pass."""
-    if t is None or isinstance(t, int):
-        return t
-    torch = _torch or _load_torch()
-    if t.dtype is not getattr(torch, dtype) or not t.is_contiguous() \
-            or (elements is not None and t.numel() != elements) \
-            or t.get_device() != _device():
-        raise _Refused
-    return t.data_ptr()
+# torch and what is used of it, looked up with the first call: these calls take a
+# few microseconds on the device, so the host's part of them counts
+_torch = _bf16 = _i32 = _f32 = _u8 = _current = _raw_stream = None
 
 
 def _device() -> int:
     """Index of the current CUDA device; -2 without one (a host tensor's is -1)."""
-    return _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -2
+    global _torch, _bf16, _i32, _f32, _u8, _current, _raw_stream
+    if _torch is None:
+        import torch
+        _bf16, _i32, _f32, _u8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+        if torch.cuda.is_available():
+            torch.cuda.init()
+            _current = torch._C._cuda_getDevice
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+        _torch = torch
+    return _current() if _current else -2
 
 
-def _rows(t: Any, B: int, N: int, heads: int, D: int):
+def _here(dev: int, *descriptors: Any) -> None:
+    """Refuses descriptors whose tensors are not on the current device."""
+    for d in descriptors:
+        if d.device is not None and d.device != dev:
+            raise _Refused
+
+
+def _dev(t: Any, dtype: Any, dev: int, elements: Optional[int] = None) -> Optional[int]:
+    """Pointer of a dense tensor of the current device with the given type (and
+    number of elements); None and raw pointers pass."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev \
+            or (elements is not None and t.numel() != elements):
+        raise _Refused
+    return t.data_ptr()
+
+
+def _rows(t: Any, dev: int, B: int, N: int, heads: int, D: int):
     """Pointer and token stride of [B][N][heads][D] bf16 rows: the values of a
     token are dense, the tokens follow each other at one stride."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t, 0
-    torch = _torch or _load_torch()
-    if t.dtype is not torch.bfloat16 or t.shape != (B, N, heads, D) \
-            or t.get_device() != _device():
+    if t.dtype is not _bf16 or t.shape != (B, N, heads, D) or t.get_device() != dev:
         raise _Refused
     if t.is_contiguous():
         return t.data_ptr(), 0
@@ -80,18 +87,9 @@ def _rows(t: Any, B: int, N: int, heads: int, D: int):
     return t.data_ptr(), step
 
 
-def _here(*descriptors: Any) -> None:
-    """Refuses descriptors whose tensors are not on the current device."""
-    for d in descriptors:
-        if d.device is not None and d.device != _device():
-            raise _Refused
-
-
-def _on(stream: Any) -> Optional[int]:
+def _on(stream: Any, dev: int) -> Optional[int]:
     """The stream's handle; None = the current stream of the current device."""
-    if stream is None and _torch is not None and _torch.cuda.is_initialized():
-        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
-    return _stream(stream)
+    return _raw_stream(dev) if stream is None and dev >= 0 else _stream(stream)
 
 
 class KvCache(ctypes.Structure):
@@ -106,12 +104,13 @@ class KvCache(ctypes.Structure):
     def of(cls, k: Any, v: Any, k_exp: Any, v_exp: Any) -> "KvCache":
         pages, Hkv, page, D = (int(n) for n in k.shape)
         rows = pages * Hkv * page
+        dev = _device()
         try:
-            c = cls(pages, page, Hkv, D, _dev(k, "uint8"), _dev(v, "uint8", rows * D),
-                    _dev(k_exp, "uint8", rows), _dev(v_exp, "uint8", rows))
+            c = cls(pages, page, Hkv, D, _dev(k, _u8, dev), _dev(v, _u8, dev, rows * D),
+                    _dev(k_exp, _u8, dev, rows), _dev(v_exp, _u8, dev, rows))
         except _Refused:
             raise StrataError(STRATA_ERR_INVALID_ARG, "KvCache") from None
-        c.tensors, c.device = (k, v, k_exp, v_exp), k.get_device()
+        c.tensors, c.device = (k, v, k_exp, v_exp), dev
         return c
 
     @classmethod
@@ -133,12 +132,13 @@ class KvSeqs(ctypes.Structure):
     @classmethod
     def of(cls, table: Any, pos: Any, count: Any = None, N: int = 1) -> "KvSeqs":
         B, max_pages = (int(n) for n in table.shape)
+        dev = _device()
         try:
-            s = cls(B, int(N), max_pages, _dev(table, "int32"), _dev(pos, "int32", B),
-                    _dev(count, "int32", B))
+            s = cls(B, int(N), max_pages, _dev(table, _i32, dev), _dev(pos, _i32, dev, B),
+                    _dev(count, _i32, dev, B))
         except _Refused:
             raise StrataError(STRATA_ERR_INVALID_ARG, "KvSeqs") from None
-        s.tensors, s.device = (table, pos, count), table.get_device()
+        s.tensors, s.device = (table, pos, count), dev
         return s
 
 
@@ -181,35 +181,38 @@ def _lib() -> ctypes.CDLL:
 def strata_kv_append(cache: KvCache, seqs: KvSeqs, k, v, stride: int = 0, stream=None) -> int:
     """k, v [B][N][Hkv][D] bf16; tensors may be parts of wider rows (their token
     stride is taken from them, `stride` is for raw pointers)."""
+    dev = _device()
     try:
-        _here(cache, seqs)
-        kp, ks = _rows(k, seqs.B, seqs.N, cache.Hkv, cache.D)
-        vp, vs = _rows(v, seqs.B, seqs.N, cache.Hkv, cache.D)
+        _here(dev, cache, seqs)
+        kp, ks = _rows(k, dev, seqs.B, seqs.N, cache.Hkv, cache.D)
+        vp, vs = _rows(v, dev, seqs.B, seqs.N, cache.Hkv, cache.D)
     except _Refused:
         return STRATA_ERR_INVALID_ARG
     if ks != vs:
         return STRATA_ERR_INVALID_ARG
-    return (_bound or _lib()).strata_kv_append(cache, seqs, kp, vp, ks or int(stride), _on(stream))
+    return (_bound or _lib()).strata_kv_append(cache, seqs, kp, vp, ks or stride, _on(stream, dev))
 
 
 def strata_kv_read(cache: KvCache, seqs: KvSeqs, k_out, v_out, stream=None) -> int:
+    dev = _device()
     n = seqs.B * seqs.N * cache.Hkv * cache.D
     try:
-        _here(cache, seqs)
-        kp, vp = _dev(k_out, "bfloat16", n), _dev(v_out, "bfloat16", n)
+        _here(dev, cache, seqs)
+        kp, vp = _dev(k_out, _bf16, dev, n), _dev(v_out, _bf16, dev, n)
     except _Refused:
         return STRATA_ERR_INVALID_ARG
-    return (_bound or _lib()).strata_kv_read(cache, seqs, kp, vp, _on(stream))
+    return (_bound or _lib()).strata_kv_read(cache, seqs, kp, vp, _on(stream, dev))
 
 
 def strata_kv_commit(cache: KvCache, seqs: KvSeqs, path, path_len, pos_out, stream=None) -> int:
+    dev = _device()
     try:
-        _here(cache, seqs)
-        a = (_dev(path, "int32", seqs.B * seqs.N), _dev(path_len, "int32", seqs.B),
-             _dev(pos_out, "int32", seqs.B))
+        _here(dev, cache, seqs)
+        a = (_dev(path, _i32, dev, seqs.B * seqs.N), _dev(path_len, _i32, dev, seqs.B),
+             _dev(pos_out, _i32, dev, seqs.B))
     except _Refused:
         return STRATA_ERR_INVALID_ARG
-    return (_bound or _lib()).strata_kv_commit(cache, seqs, *a, _on(stream))
+    return (_bound or _lib()).strata_kv_commit(cache, seqs, *a, _on(stream, dev))
 
 
 def strata_tree_attention_workspace_bytes(cache: KvCache, seqs: KvSeqs, Hq: int) -> int:
@@ -230,32 +233,36 @@ def strata_tree_attention(cache: KvCache, seqs: KvSeqs, parent, q, scale, out, w
                           q_stride: int = 0, stream=None) -> int:
     """q, out [B][N][Hq][D] bf16, parent [B][N] int32 or None; a q tensor may be a
     part of wider rows.  Hq and q_stride are for raw pointers."""
+    dev = _device()
     B, N, D = seqs.B, seqs.N, cache.D
     try:
-        _here(cache, seqs)
-        if not isinstance(q, int) and q is not None:
-            Hq = int(q.shape[2]) if q.dim() == 4 else 0
+        _here(dev, cache, seqs)
+        if q is not None and q.__class__ is not int:
+            Hq = q.shape[2] if q.dim() == 4 else 0
         heads = int(Hq or 0)
-        qp, qs = _rows(q, B, N, heads, D)
-        op, pp = _dev(out, "bfloat16", B * N * heads * D), _dev(parent, "int32", B * N)
-        wp = _dev(ws, "uint8")
+        qp, qs = _rows(q, dev, B, N, heads, D)
+        op, pp = _dev(out, _bf16, dev, B * N * heads * D), _dev(parent, _i32, dev, B * N)
+        wp = _dev(ws, _u8, dev)
     except _Refused:
         return STRATA_ERR_INVALID_ARG
     return (_bound or _lib()).strata_tree_attention(
-        cache, seqs, pp, qp, qs or int(q_stride), heads, float(scale), op, wp,
-        _nbytes(ws) if ws_bytes is None else int(ws_bytes), _on(stream))
+        cache, seqs, pp, qp, qs or q_stride, heads, scale, op, wp,
+        _nbytes(ws) if ws_bytes is None else ws_bytes, _on(stream, dev))
 
 
 def strata_verify_drafts(tokens, parent, count, p, q, u_accept, u_sample, dims, path, path_len,
                          out_tokens, stream=None) -> int:
+    dev = _device()
     d = VerifyDims.of(dims)
-    nodes, probs = d.B * d.N, d.B * d.N * d.V
+    B = d.B
+    nodes = B * d.N
+    probs = nodes * d.V
     try:
-        a = [_dev(tokens, "int32", nodes), _dev(parent, "int32", nodes), _dev(count, "int32", d.B),
-             _dev(p, "float32", probs), _dev(q, "float32", probs),
-             _dev(u_accept, "float32", nodes), _dev(u_sample, "float32", d.B)]
-        o = [_dev(path, "int32", nodes), _dev(path_len, "int32", d.B),
-             _dev(out_tokens, "int32", nodes)]
+        a = (_dev(tokens, _i32, dev, nodes), _dev(parent, _i32, dev, nodes),
+             _dev(count, _i32, dev, B), _dev(p, _f32, dev, probs), _dev(q, _f32, dev, probs),
+             _dev(u_accept, _f32, dev, nodes), _dev(u_sample, _f32, dev, B), d,
+             _dev(path, _i32, dev, nodes), _dev(path_len, _i32, dev, B),
+             _dev(out_tokens, _i32, dev, nodes))
     except _Refused:
         return STRATA_ERR_INVALID_ARG
-    return (_bound or _lib()).strata_verify_drafts(*a, d, *o, _on(stream))
+    return (_bound or _lib()).strata_verify_drafts(*a, _on(stream, dev))
