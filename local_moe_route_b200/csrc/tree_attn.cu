@@ -83,15 +83,16 @@ __host__ __device__ constexpr uint32_t unit_cost(uint32_t tiles, uint32_t ctas) 
 }
 constexpr int UNITS = 4;                    // units announced ahead
 constexpr int C = 16;                       // row columns per softmax warpgroup
+constexpr int CTAS = 2;                     // per SM
 
 template <int D, int R>
 struct Cfg {
   static constexpr int NWG = R / C;                    // softmax warpgroups
-  static constexpr int CTAS = R == 64 ? 1 : 2;         // per SM
   // K and V rings, in MMA tiles
-  static constexpr int KS = (R == 64 ? 4 : 2) * (D == 64 ? 2 : 1);
-  static constexpr int VS = (R == 64 ? 4 : 2) * (D == 64 ? 2 : 1);
-  static constexpr int ES = KS / 2 + 2;                // exponents, in softmax tiles
+  static constexpr int KS = D == 64 ? 4 : 2;
+  static constexpr int VS = D == 64 ? 4 : 2;
+  static constexpr int ES = 4;                         // exponents, in softmax tiles
+  static_assert(ES >= KS / 2 + 2, "see load_e");
   static constexpr int SOFT = NWG * 128;
   static constexpr int THREADS = SOFT + 64;
   static constexpr int KV_BYTES = SUB * D;             // one operand tile
@@ -103,7 +104,7 @@ struct Cfg {
   static constexpr int E_OFF = P_OFF + TILE * 2 * R;           // [ES][K, V][TILE] exponents
   static constexpr int MISC_OFF = E_OFF + ES * 2 * TILE;
   static constexpr int O_COL = 4 * R;                  // TMEM: the scores, then O
-  static constexpr int TMEM_COLS = R == 64 ? 512 : R == 32 ? 256 : 128;
+  static constexpr int TMEM_COLS = R == 32 ? 256 : 128;
 };
 
 // One unit as a run sees it: tiles first .. stop - 1 of (sequence, KV head,
@@ -120,7 +121,7 @@ struct Misc {
   uint64_t k_full[F::KS], k_empty[F::KS], v_full[F::VS], v_empty[F::VS], e_full[F::ES];
   uint64_t s_full, s_free, p_ready, o_full, q_full, qr_full, qr_empty;
   uint64_t u_full[UNITS], u_empty[UNITS];
-  uint32_t seen_by[NODES][2];        // rows that see the node
+  uint32_t seen_by[NODES];           // rows that see the node
   unsigned long long nan_nodes;      // nodes whose V holds a NaN
   Unit unit[UNITS];
   uint32_t tmem;
@@ -417,7 +418,7 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t n) {
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
+__global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
     tree_attn_kernel(const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const TreeArgs a) {
   using namespace ta;
@@ -603,20 +604,16 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         return false;
       if (some) {
         const bool drafts = (unsigned)u.stop * TILE > (unsigned)u.pos;
-        uint32_t n = 0;
-        int node[(R + 31) / 32], row_q[(R + 31) / 32];
-#pragma unroll
-        for (int k = 0; k < (R + 31) / 32; ++k) {
-          const int r = k * 32 + lane, flat = u.rb * R + r;
-          node[k] = flat / a.G;
-          row_q[k] = node[k] * a.Hq + u.hk * a.G + flat - node[k] * a.G;
-          if (r < R) {
-            m.row_node[us][r] = node[k];
-            m.row[us][r] = row_q[k];
-          }
-          if (r >= R) node[k] = u.count;
-          n += __popc(__ballot_sync(0xffffffffu, node[k] < u.count));
+        const int flat = u.rb * R + lane;              // R <= 32: a row per lane
+        int node = flat / a.G;
+        const int head = u.hk * a.G + flat - node * a.G, row_q = node * a.Hq + head;
+        if (lane < R) {
+          m.row_node[us][lane] = node;
+          m.row[us][lane] = row_q;
+        } else {
+          node = u.count;
         }
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, node < u.count));
         int up[NODES / 32];
 #pragma unroll
         for (int j = 0; j < NODES / 32; ++j) {
@@ -628,13 +625,10 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         if (lane == 0) mbar_arrive_expect_tx(&m.qr_full, n * D * 2);
         __syncwarp();
         ++nq;
-#pragma unroll
-        for (int k = 0; k < (R + 31) / 32; ++k)
-          if (node[k] < u.count)
-            bulk_load(smem + F::QR_OFF + (k * 32 + lane) * D * 2,
-                      a.q + ((int64_t)u.b * a.s.N + node[k]) * a.q_stride +
-                          (int64_t)(row_q[k] - node[k] * a.Hq) * D,
-                      D * 2, &m.qr_full);
+        if (node < u.count)
+          bulk_load(smem + F::QR_OFF + lane * D * 2,
+                    a.q + ((int64_t)u.b * a.s.N + node) * a.q_stride + (int64_t)head * D, D * 2,
+                    &m.qr_full);
 #pragma unroll
         for (int j = 0; j < NODES / 32; ++j) {
           const int i = j * 32 + lane;
@@ -842,7 +836,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         nan_nodes &= nan_nodes - 1;
         const int64_t row = row_of(a.c, a.s, u.b, (int64_t)u.pos + j) + (int64_t)u.hk * a.c.page;
         const bool nan = has_feat && (a.c.v[row * D + feat] & 0x7F) == 0x7F;
-        const uint32_t by = m.seen_by[j][wg * C / 32] >> (wg * C % 32);
+        const uint32_t by = m.seen_by[j] >> (wg * C);
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (nan && ((by >> c) & 1)) o[c] = __uint_as_float(0x7FC00000u);
@@ -872,7 +866,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       if (u.last) break;
       const unsigned pos = (unsigned)u.pos;
       const bool drafts = (unsigned)u.stop * TILE > pos;     // the run reaches the tree
-      if (th < NODES) m.seen_by[th][0] = m.seen_by[th][1] = 0;
+      if (th < NODES) m.seen_by[th] = 0;
       if (th == 0) m.nan_nodes = 0;
       ok = ta_wait(&m.qr_full, un & 1, abort_flag, a.err) && ok;
       constexpr int LPR = D / 8;             // lanes per row, 8 values each
@@ -919,7 +913,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
       if (!dead && drafts) {
         if (th < R)
           for (int j = min(m.row_node[us][th], NODES - 1); j >= 0; j = m.parent[us][j])
-            atomicOr(&m.seen_by[j][th / 32], 1u << (th % 32));
+            atomicOr(&m.seen_by[j], 1u << th);
         named_barrier_sync(1, ALL);
       }
       if (th == 0) mbar_arrive(&m.qr_empty);
@@ -945,7 +939,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
             if (t >= end || ke[h] == 0)
               vis[h] = 0;
             else if (t >= pos)
-              vis[h] = m.seen_by[t - pos][wg * C / 32] >> (wg * C % 32);
+              vis[h] = m.seen_by[t - pos] >> (wg * C);
           }
         }
         ok = ta_wait(&m.s_full, g & 1, abort_flag, a.err) && ok;
@@ -1001,8 +995,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
               __reduce_max_sync(0xffffffffu, max(vis[0] ? ve[0] : 0u, vis[1] ? ve[1] : 0u));
           if (lane == 0) m.wtop[wg][wq] = w;
         }
-        dead = named_barrier_or(bar_wg, 128, !ok);
-        if (dead) break;
+        named_barrier_sync(bar_wg, 128);
         const uint32_t etop = tree ? 0u
                                    : max(max(m.wtop[wg][0], m.wtop[wg][1]),
                                          max(m.wtop[wg][2], m.wtop[wg][3]));
@@ -1011,11 +1004,11 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
           const float top = fmaxf(fmaxf(m.wmax[wg][0][lt], m.wmax[wg][1][lt]),
                                   fmaxf(m.wmax[wg][2][lt], m.wmax[wg][3][lt]));
           uint32_t ex = etop;
-          if (tree) {
+          if (tree)
             ex = max(max(m.wexp[wg][0][lt], m.wexp[wg][1][lt]),
                      max(m.wexp[wg][2][lt], m.wexp[wg][3][lt]));
-            m.eh[wg][lt] = ex < 254u ? __uint_as_float((254u - ex) << 23) : __uint_as_float(1u << 22);
-          }
+          // 2^(127 - ex); 2^-127 is subnormal
+          m.eh[wg][lt] = ex < 254u ? __uint_as_float((254u - ex) << 23) : __uint_as_float(1u << 22);
           // a tile without a visible position changes nothing
           const float ref = top == -INFINITY ? (m_run == -INFINITY ? 0.f : m_run) : ceilf(top);
           const float now = top == -INFINITY ? m_run : fmaxf(m_run, ref);
@@ -1031,7 +1024,9 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
           m.beta[wg][lt] = pow2i(d);
           m.beta_o[wg][g & 1][lt] = pow2i(d + (int)ex - 127);
         }
-        const bool rescale = named_barrier_or(bar_wg, 128, moved);
+        // (the references, and whether any moved or a wait gave up)
+        const bool rescale = named_barrier_or(bar_wg, 128, moved || !ok);
+        if (rescale && (dead = named_barrier_or(bar_wg, 128, !ok))) break;
         // weights; their sums per position in l, scaled to the running maximum
         if (rescale) {
 #pragma unroll
@@ -1068,14 +1063,14 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::Cfg<D, R>::CTAS)
         float vf[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          // 2^(ev - E of the row); above 1 only where the weight is 0
+          const float f = __uint_as_float(ve[h] << 23);
           if (tree) {
-            // 2^(ev - E of the row); above 1 only where the weight is 0
-            const float f = __uint_as_float(ve[h] << 23);
 #pragma unroll
             for (int c = 0; c < C; ++c) s[h][c] *= fminf(f * m.eh[wg][c], 1.f);
             vf[h] = WSCALE;
           } else {
-            vf[h] = pow2i(min((int)ve[h] - (int)etop, 0)) * WSCALE;
+            vf[h] = fminf(f * m.eh[wg][0], 1.f) * WSCALE;
           }
 #pragma unroll
           for (int c = 0; c < C; c += 2) {
@@ -1327,14 +1322,13 @@ __global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a
 
 static int tree_block_rows(int N, int G) {
   const int rows = N * G;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 16 ? 16 : 32;
 }
 
 // CTAs on `sms` SMs, as many as the workspace has room for at most.
-static int tree_ctas(int R, int sms) {
-  const int n = sms * (R == 64 ? 1 : 2);
-  const int room = ta::MAX_CTAS / (R == 64 ? 2 : 1);
-  return n < room ? n : room;
+static int tree_ctas(int sms) {
+  const int n = sms * ta::CTAS;
+  return n < ta::MAX_CTAS ? n : ta::MAX_CTAS;
 }
 static int tree_blocks(int N, int G) {
   const int R = tree_block_rows(N, G);
@@ -1348,7 +1342,7 @@ static size_t tree_heads_bytes(const strata_kv_cache_t& c, const strata_kv_seqs_
 size_t tree_attn_scratch(const strata_kv_cache_t& c, const strata_kv_seqs_t& s, int Hq) {
   const int R = tree_block_rows(s.N, Hq / c.Hkv);
   return tree_heads_bytes(c, s, Hq) +
-         (size_t)tree_ctas(R, ta::MAX_CTAS) * 2 * ta::slot_floats(R, c.D) * sizeof(float);
+         (size_t)ta::MAX_CTAS * 2 * ta::slot_floats(R, c.D) * sizeof(float);
 }
 
 template <int D, int R>
@@ -1356,12 +1350,11 @@ static cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const C
                                cudaStream_t stream) {
   using F = ta::Cfg<D, R>;
   constexpr int SMEM = F::MISC_OFF + (int)sizeof(ta::Misc<F, R>);
-  static_assert(SMEM <= 232448, "shared memory");
-  static_assert(F::CTAS == 1 || 2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
+  static_assert(ta::CTAS * (SMEM + 1024) <= 233472, "two CTAs per SM");
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, R>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  const int grid = tree_ctas(R, sm_count());
+  const int grid = tree_ctas(sm_count());
   tree_attn_kernel<D, R><<<grid, F::THREADS, SMEM, stream>>>(mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1409,12 +1402,8 @@ cudaError_t launch_tree_attn(const strata_kv_cache_t& c, const strata_kv_seqs_t&
     return cudaErrorInvalidValue;
   const int R = tree_block_rows(s.N, a.G);
   if (c.D == 128)
-    return R == 16 ? launch_tree<128, 16>(a, mk, mv, stream)
-           : R == 32 ? launch_tree<128, 32>(a, mk, mv, stream)
-                     : launch_tree<128, 64>(a, mk, mv, stream);
-  return R == 16 ? launch_tree<64, 16>(a, mk, mv, stream)
-         : R == 32 ? launch_tree<64, 32>(a, mk, mv, stream)
-                   : launch_tree<64, 64>(a, mk, mv, stream);
+    return R == 16 ? launch_tree<128, 16>(a, mk, mv, stream) : launch_tree<128, 32>(a, mk, mv, stream);
+  return R == 16 ? launch_tree<64, 16>(a, mk, mv, stream) : launch_tree<64, 32>(a, mk, mv, stream);
 }
 
 }  // namespace strata
