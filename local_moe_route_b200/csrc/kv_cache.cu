@@ -24,36 +24,51 @@ __device__ __forceinline__ float pow2_biased(int biased) {   // 2^(biased - 127)
   return __uint_as_float((uint32_t)biased << 23);
 }
 
+// Biased exponent of a row whose largest magnitude has the bf16 bits `top`:
+// 448 = 1.75 * 2^8, so mantissas above 1.75 take the next exponent.
+__device__ __forceinline__ int row_exponent(uint32_t top) {
+  const int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
+  return min(max(e, -126), 119) + 127;
+}
+
 // Sixteen bf16 values per lane, D / 16 lanes per row: codes (16 bytes) and the
-// row's biased exponent.
+// row's biased exponent.  Called by whole warps.  Two 16-bit maxima per
+// instruction and two scaled values per multiplication: with one value at a time
+// and the infinities looked for in each, the kernel was bound by this
+// arithmetic (four 6144-token chunks 18.0 us).
 template <int D>
 __device__ __forceinline__ uint4 quantise16(const uint4& x0, const uint4& x1, int* biased) {
   const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-  // largest finite magnitude, as bf16 bits
-  uint32_t top = 0;
+  uint32_t top2 = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-    top = max(top, lo < 0x7F80u ? lo : 0u);
-    top = max(top, hi < 0x7F80u ? hi : 0u);
+  for (int i = 0; i < 8; ++i) top2 = __vmaxu2(top2, w[i] & 0x7FFF7FFFu);
+  uint32_t top = max(top2 >> 16, top2 & 0xFFFFu);
+  const bool odd = __any_sync(0xffffffffu, top >= 0x7F80u);   // an infinity or a NaN
+  if (odd) {                             // the largest finite magnitude
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+      top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+    }
   }
 #pragma unroll
   for (int off = D / 32; off > 0; off >>= 1)
     top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-  // 448 = 1.75 * 2^8: mantissas above 1.75 take the next exponent
-  int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
-  e = min(max(e, -126), 119);
-  *biased = e + 127;
-  const float s = pow2_biased(127 - e);
+  *biased = row_exponent(top);
+  const float f = pow2_biased(254 - *biased);
   uint32_t c[4];
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     c[h] = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float a = bf16_lo(w[2 * h + j]), b = bf16_hi(w[2 * h + j]);
-      // 0 * x is NaN for an infinity (which has no code) and 0 otherwise
-      const float2 y = make_float2(fmaf(a, s, 0.f * a), fmaf(b, s, 0.f * b));
+      const uint32_t v = w[2 * h + j];
+      float2 y = __fmul2_rn(make_float2(bf16_lo(v), bf16_hi(v)), make_float2(f, f));
+      if (odd) {                         // infinities have no code: NaN, as 0 * x says
+        y.x += 0.f * bf16_lo(v);
+        y.y += 0.f * bf16_hi(v);
+      }
       c[h] |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * j);
     }
   }
@@ -99,57 +114,51 @@ __device__ __forceinline__ int64_t token_pos(const strata_kv_seqs_t& s, int tok,
 }
 
 // Bound by its bytes once there are tens of thousands of rows, by the chain
-// position -> page -> row below; two steps' loads are in flight while the page
-// is looked up (their addresses do not depend on it).  More tokens per
-// warp in place of more warps was slower (four 6144-token chunks, 8 rows a
-// token: 17.2, 19.0 and 19.3 us with 1, 2 and 4).
+// position -> page -> row below; the rows' loads are in flight while the page is
+// looked up (their addresses do not depend on it).  Four 6144-token chunks (57 MB)
+// take 15.5 us, 3.7 TB/s; two steps in flight per warp 16.3 us (more registers,
+// fewer warps), two tokens per warp 10 % more.
 template <int D>
 __global__ void __launch_bounds__(kvc::THREADS)
     kv_append_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, const uint16_t* __restrict__ k,
                      const uint16_t* __restrict__ v, int64_t stride, unsigned* err) {
-  constexpr int U = 2;
   const RowLanes<D> w(c, s);
   int b = 0;
   const int64_t pos = token_pos(s, w.tok, &b, err);
   const int rows = 2 * c.Hkv;
   int64_t row = -1;
-  for (int r0 = 0; r0 < rows; r0 += U * w.step) {
-    uint4 x[U][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * w.step + w.r;
-      x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-      if (r < rows && pos >= 0) {
-        const uint16_t* src = (r >= c.Hkv ? v + (int64_t)(r - c.Hkv) * D : k + (int64_t)r * D) +
-                              w.tok * stride + w.ch * 16;
-        x[u][0] = ld_nc_v4(src);
-        x[u][1] = ld_nc_v4(src + 8);
-      }
+  for (int r0 = 0; r0 < rows; r0 += w.step) {
+    const int r = r0 + w.r;
+    const bool is_v = r >= c.Hkv;
+    const int h = is_v ? r - c.Hkv : r;
+    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (r < rows && pos >= 0) {
+      const uint16_t* src = (is_v ? v : k) + w.tok * stride + (int64_t)h * D + w.ch * 16;
+      x[0] = ld_nc_v4(src);
+      x[1] = ld_nc_v4(src + 8);
     }
     if (r0 == 0 && pos >= 0) {
       row = row_of(c, s, b, pos);
       if (row < 0) atomicOr(err, kErrIndex);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * w.step + w.r;
-      int biased;
-      const uint4 code = quantise16<D>(x[u][0], x[u][1], &biased);
-      if (r >= rows || row < 0) continue;
-      const bool is_v = r >= c.Hkv;
-      const int64_t at = row + (int64_t)(is_v ? r - c.Hkv : r) * c.page;
-      *reinterpret_cast<uint4*>((is_v ? c.v : c.k) + at * D + w.ch * 16) = code;
-      if (w.ch == 0) (is_v ? c.v_exp : c.k_exp)[at] = (uint8_t)biased;
-    }
+    int biased;
+    const uint4 code = quantise16<D>(x[0], x[1], &biased);
+    if (r >= rows || row < 0) continue;
+    const int64_t at = row + (int64_t)h * c.page;
+    *reinterpret_cast<uint4*>((is_v ? c.v : c.k) + at * D + w.ch * 16) = code;
+    if (w.ch == 0) (is_v ? c.v_exp : c.k_exp)[at] = (uint8_t)biased;
   }
 }
 
 __device__ __forceinline__ uint32_t dequantise2(uint32_t codes, float f) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-  const float2 y = __half22float2(__half2(h));
-  return pack_bf16x2(y.x * f, y.y * f);
+  const float2 y = __fmul2_rn(__half22float2(__half2(h)), make_float2(f, f));
+  return pack_bf16x2(y.x, y.y);
 }
 
+// 34,000 positions at 4 heads (105 MB, two thirds of them written) take 22.4 us,
+// 4.7 TB/s; 8 values per lane with contiguous stores, or one or four steps in
+// flight instead of two, were no faster.
 template <int D>
 __global__ void __launch_bounds__(kvc::THREADS)
     kv_read_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, uint16_t* __restrict__ k_out,
