@@ -45,9 +45,11 @@
 // different times (after the scores, after the output), so they are separate
 // rings; the next tile's scores are issued as soon as these have left TMEM.
 //
-// R, the rows per block, is 16, 32 or 64: the smallest that holds all rows of
-// N nodes, 64 at most (the instruction's width is 2R = 128, and the sums of 64 rows
-// need 4 warpgroups' registers).  Two CTAs per SM at R <= 32, one at 64 (TMEM).
+// R, the rows per block, is 16 when all rows of N nodes fit and 32 otherwise,
+// with two CTAs per SM (their TMEM and registers).  Blocks of 64 rows (one CTA per
+// SM) were 5 % faster on 64-node trees of 4 sequences (72 against 75 us) and 10 to
+// 20 % slower on 8-node and on few trees; blocks of 16 for all rows 36 % slower on
+// 24-node trees.
 //
 // Measured (D = 128, 4 KV heads, 32 query heads, one call, burst clocks): 32
 // sequences of 4 nodes behind up to 34,000 positions 108 us, 5.4 TB/s of the
@@ -56,7 +58,7 @@
 // are the launch, 6 us the first tile's chain of dependent steps (lengths -> page
 // -> copy -> scores) and 2 us the join.  In a long line a tile takes a CTA
 // 3.3 us, with two CTAs per SM near what its 66 KB take at the copy rate; D = 64
-// halves the bytes but not the arithmetic (100 us): the softmax warps then issue
+// halves the bytes but not the arithmetic (98 us): the softmax warps then issue
 // about half of the time and wait for each other the rest.  Steps that did not
 // help: the last fifth of the line in small runs taken from a counter (141 us
 // against 126: a run costs two tiles), one barrier per tile with every warp
@@ -133,7 +135,7 @@ struct Misc {
   uint32_t start_off;
   int start_b;
   int nan_row[R];
-  alignas(16) float qf[R];                       // score factor of the row
+  alignas(16) float qf[R];                    // score factor of the row
   alignas(16) float wmax[F::NWG][4][C];       // per warp: largest score of the tile
   alignas(16) uint32_t wexp[F::NWG][4][C];    // per warp: largest visible V exponent
   uint32_t wtop[F::NWG][4];
@@ -141,7 +143,7 @@ struct Misc {
   alignas(16) float beta_o[F::NWG][2][C];
   alignas(16) float eh[F::NWG][C];            // a row's V exponent as a factor
   alignas(16) float lsum[F::NWG][4][C];       // per warp: sums of the weights
-  alignas(16) float inv[R];                      // 1 / (sum * WSCALE)
+  alignas(16) float inv[R];                   // 1 / (sum * WSCALE)
 };
 
 // A run's first unit may have begun in an earlier run: slot 0; its last may go
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
     };
     // The slot's last tile is done with: this warp has waited until the K tile
     // KS / 2 tiles back was read, which comes after the weights KS / 2 + 2 tiles
-    // back were finished.
+    // back were finished (ES >= KS / 2 + 2).
     auto load_e = [&]() {
       const int es = g % ES;
       uint8_t* e = sE + es * 2 * TILE + lane * page;
