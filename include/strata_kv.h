@@ -110,7 +110,8 @@ STRATA_API strata_status_t strata_kv_read(strata_kv_cache_t cache, strata_kv_seq
  *            < 2^31
  *   scale    <= 0 means 1 / sqrt(D)
  *   out      [B][N][Hq][D] bf16; rows of slots behind count[b] are left as they
- *            were; a node that sees no row gets zeros
+ *            were; a node that sees no row gets zeros; may be q itself
+ *            (q_stride = Hq * D)
  * Values at positions a node does not see, NaN among them, do not reach it.
  * Scores, softmax and sums in fp32; for the product with V the weights of a tile
  * of 256 positions are rounded to 2^-9 of their value, or to 2^-17.8 of the

@@ -102,6 +102,8 @@ class KvCache(ctypes.Structure):
 
     @classmethod
     def of(cls, k: Any, v: Any, k_exp: Any, v_exp: Any) -> "KvCache":
+        if k.dim() != 4:
+            raise StrataError(STRATA_ERR_INVALID_ARG, "KvCache")
         pages, Hkv, page, D = (int(n) for n in k.shape)
         rows = pages * Hkv * page
         dev = _device()
@@ -131,6 +133,8 @@ class KvSeqs(ctypes.Structure):
 
     @classmethod
     def of(cls, table: Any, pos: Any, count: Any = None, N: int = 1) -> "KvSeqs":
+        if table.dim() != 2:
+            raise StrataError(STRATA_ERR_INVALID_ARG, "KvSeqs")
         B, max_pages = (int(n) for n in table.shape)
         dev = _device()
         try:

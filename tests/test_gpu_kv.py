@@ -603,3 +603,67 @@ def test_attention_keeps_a_sink_and_a_long_tail_apart(dev):
     off = 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -11 + 255 * 2.0 ** -17.8
     assert abs(got[0] - 0.75) <= 0.75 * off and abs(got[1] - 0.25) <= 0.25 * (2.0 ** -8 + 2.0 ** -9
                                                                           + 2.0 ** -11) + 255 * 2.0 ** -17.8
+
+
+def test_attention_of_positions_behind_the_page_table(dev):
+    """A committed length past the table's room: what has a column is attended to,
+    the rest (the nodes too) reported and passed over."""
+    rng = np.random.default_rng(92)
+    a = Setup(rng, dev, [48, 512, 300], None, 2, 2, 64, 16)
+    a.table = a.table[:, :3].copy()                  # room for 48 positions
+    a.pos = np.array([48, 1000, 40], np.int32)
+    a.upload(dev)
+    q = bf16_bits(rng.standard_normal((3, 2, 4, 64)).astype(np.float32))
+    out = run_attention(a, None, q, dev)
+    assert sm.strata_moe_device_status() == sm.STRATA_ERR_DEVICE_CHECK
+    check_attention(a, None, q, out)
+
+
+def test_attention_of_thousands_of_short_sequences(dev):
+    rng = np.random.default_rng(93)
+    B = 3000
+    pos = rng.integers(0, 3, B)
+    count = rng.integers(0, 3, B)
+    a = Setup(rng, dev, pos, count, 2, 1, 64, 16)
+    q = bf16_bits(rng.standard_normal((B, 2, 2, 64)).astype(np.float32))
+    out = run_attention(a, None, q, dev)
+    assert_device_ok()
+    check_attention(a, None, q, out)
+
+
+def test_attention_in_place_and_with_shared_pages(dev):
+    """Two sequences that share their first pages, and the output written over the
+    queries."""
+    rng = np.random.default_rng(94)
+    a = Setup(rng, dev, [600, 600], None, 4, 2, 128, 32)
+    a.table[1, :18] = a.table[0, :18]                # positions below 576 are the same
+    a.upload(dev)
+    q = bf16_bits(rng.standard_normal((2, 4, 8, 128)).astype(np.float32))
+    out = run_attention(a, None, q, dev)
+    same = up_bf16(q, dev)
+    ws = sm.tree_attention_workspace(a.c, a.s, 8, dev)
+    sm.check(sm.strata_tree_attention(a.c, a.s, None, same, 0.0, same, ws))
+    assert_device_ok()
+    check_attention(a, None, q, out)
+    assert torch.equal(same, out)
+
+
+def test_one_workspace_for_two_captured_calls(dev):
+    rng = np.random.default_rng(95)
+    a = Setup(rng, dev, [700, 10], None, 3, 2, 64, 16)
+    b = Setup(rng, dev, [5, 1200], None, 3, 2, 64, 16)
+    q = bf16_bits(rng.standard_normal((2, 3, 8, 64)).astype(np.float32))
+    want = [run_attention(x, None, q, dev) for x in (a, b)]
+    ws = torch.empty(max(sm.strata_tree_attention_workspace_bytes(x.c, x.s, 8) for x in (a, b)),
+                     dtype=torch.uint8, device=dev)
+    qd, outs, graphs = up_bf16(q, dev), [torch.zeros_like(w) for w in want], []
+    for x, o in zip((a, b), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sm.check(sm.strata_tree_attention(x.c, x.s, None, qd, 0.0, o, ws))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want[i])

@@ -97,6 +97,34 @@ def test_verify_sizes_counts_and_many_rejections(dev):
     check(d, run(d, dev))
 
 
+def test_verify_past_two_to_the_31_values(dev):
+    """Rows whose offsets pass 32 bits."""
+    B, N, V = 65, 64, 600001
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB of free device memory")
+    rng = np.random.default_rng(12)
+    a = make(rng, 1, 5, V, "star")
+    p = torch.zeros((B, N, V), device=dev)
+    p[-1, :5] = up(a["p"][0], dev)
+    t = {k: np.zeros((B, N), x.dtype) for k, x in a.items() if k in ("tokens", "u_accept")}
+    for k in t:
+        t[k][-1, :5] = a[k][0]
+    parent = np.full((B, N), -1, np.int32)
+    parent[-1, :5] = a["parent"][0]
+    count = np.zeros(B, np.int32)
+    count[-1] = 5
+    us = np.zeros(B, np.float32)
+    us[-1] = a["u_sample"][0]
+    out = [torch.full(s, -9, dtype=torch.int32, device=dev) for s in ((B, N), (B,), (B, N))]
+    sm.check(sm.strata_verify_drafts(up(t["tokens"], dev), up(parent, dev), up(count, dev), p, None,
+                                     up(t["u_accept"], dev), up(us, dev), (B, N, V), *out))
+    assert_device_ok()
+    want = osp.verify(a["tokens"], a["parent"], None, a["p"], None, a["u_accept"], a["u_sample"])
+    assert np.array_equal(out[0][-1, :5].cpu().numpy(), want[0][0])
+    assert out[1].cpu().tolist() == [0] * (B - 1) + [int(want[1][0])]
+    assert np.array_equal(out[2][-1, :5].cpu().numpy(), want[2][0])
+
+
 def test_verify_equal_rows_and_extreme_random_numbers(dev):
     """p = q accepts everything; u_sample 0 takes the lowest token with any
     probability, u_sample next to 1 the highest; sums on exact borders go to the next

@@ -162,6 +162,10 @@ def test_binding_refuses_host_tensors_and_other_layouts():
         KvCache.of(z(2, 2, 16, 64), z(2, 2, 16, 64), z(2, 2, 16), z(2, 2, 16))
     with pytest.raises(sm.StrataError):
         KvSeqs.of(z(2, 3, t=torch.int32), z(2, t=torch.int32))
+    with pytest.raises(sm.StrataError):
+        KvCache.of(z(2, 2, 64), z(2, 2, 64), z(2, 2, 16), z(2, 2, 16))
+    with pytest.raises(sm.StrataError):
+        KvSeqs.of(z(6, t=torch.int32), z(2, t=torch.int32))
     x = z(2, 4, 2, 64, t=torch.bfloat16)
     assert append(k=x, v=x) == INVALID
     assert sm.strata_kv_read(cache(), seqs(), x, x, stream=0) == INVALID
