@@ -33,6 +33,57 @@ cudaError_t launch_verify(const int32_t* tokens, const int32_t* parent, const in
                           cudaStream_t stream);
 
 #ifdef __CUDACC__
+// These kernels are launched so that their CTAs may be set up while the kernel
+// before them in the stream still runs (programmatic stream serialization): a
+// step is a chain of calls of a few microseconds each, and the gap between two
+// launches is about one.  Every kernel waits, in all its threads and before it
+// touches global memory, until the kernel before it is complete and its writes
+// are visible, so the order of the stream's work is what it always is; it lets the
+// next one in as soon as all its own CTAs run.  What another kernel may have
+// written is read with plain loads: the read-only path asks for data that does not
+// change while the kernel is resident, and it may be resident early.  Calls of one
+// token per sequence one after another from Python: append 8.1 -> 7.5 us, attention
+// 12.4 -> 11.2; in a graph 2.7 -> 2.6 and 11.1 -> 11.0.
+__device__ __forceinline__ void stream_order_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void stream_order_begin() {
+  stream_order_wait();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
+// `cluster`: CTAs per cluster along x, 0 when the kernel says it itself.
+template <class... P, class... A>
+inline cudaError_t launch_in_order(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                                   cudaStream_t stream, unsigned cluster, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {cluster, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // The first position and the number of tokens of sequence b in this call; a
 // negative position or a count outside 0 .. N leaves it without tokens.
 struct SeqRange {

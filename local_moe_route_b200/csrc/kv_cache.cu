@@ -116,12 +116,13 @@ __device__ __forceinline__ int64_t token_pos(const strata_kv_seqs_t& s, int tok,
 // Bound by its bytes once there are tens of thousands of rows, by the chain
 // position -> page -> row below; the rows' loads are in flight while the page is
 // looked up (their addresses do not depend on it).  Four 6144-token chunks (57 MB)
-// take 15.5 us, 3.7 TB/s; two steps in flight per warp 16.3 us (more registers,
+// take 14.7 us, 3.9 TB/s; two steps in flight per warp 16.3 us (more registers,
 // fewer warps), two tokens per warp 10 % more.
 template <int D>
 __global__ void __launch_bounds__(kvc::THREADS)
-    kv_append_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, const uint16_t* __restrict__ k,
-                     const uint16_t* __restrict__ v, int64_t stride, unsigned* err) {
+    kv_append_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, const uint16_t* k, const uint16_t* v,
+                     int64_t stride, unsigned* err) {
+  stream_order_begin();
   const RowLanes<D> w(c, s);
   int b = 0;
   const int64_t pos = token_pos(s, w.tok, &b, err);
@@ -134,8 +135,8 @@ __global__ void __launch_bounds__(kvc::THREADS)
     uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (r < rows && pos >= 0) {
       const uint16_t* src = (is_v ? v : k) + w.tok * stride + (int64_t)h * D + w.ch * 16;
-      x[0] = ld_nc_v4(src);
-      x[1] = ld_nc_v4(src + 8);
+      x[0] = ld_v4(src);
+      x[1] = ld_v4(src + 8);
     }
     if (r0 == 0 && pos >= 0) {
       row = row_of(c, s, b, pos);
@@ -156,14 +157,15 @@ __device__ __forceinline__ uint32_t dequantise2(uint32_t codes, float f) {
   return pack_bf16x2(y.x, y.y);
 }
 
-// 34,000 positions at 4 heads (105 MB, two thirds of them written) take 22.4 us,
+// 34,000 positions at 4 heads (105 MB, two thirds of them written) take 22.6 us,
 // 4.7 TB/s; 8 values per lane with contiguous stores, or one or four steps in
 // flight instead of two, were no faster.
 template <int D>
 __global__ void __launch_bounds__(kvc::THREADS)
-    kv_read_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, uint16_t* __restrict__ k_out,
-                   uint16_t* __restrict__ v_out, unsigned* err) {
+    kv_read_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, uint16_t* k_out, uint16_t* v_out,
+                   unsigned* err) {
   constexpr int U = 2;
+  stream_order_begin();
   const RowLanes<D> w(c, s);
   int b = 0;
   const int64_t pos = token_pos(s, w.tok, &b, err);
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kvc::THREADS)
       if (out[u] && row >= 0) {
         const int64_t at = row + (int64_t)h * c.page;
         e[u] = (is_v ? c.v_exp : c.k_exp)[at];
-        code[u] = ld_nc_v4((is_v ? c.v : c.k) + at * D + w.ch * 16);
+        code[u] = ld_v4((is_v ? c.v : c.k) + at * D + w.ch * 16);
       }
       if (out[u]) out[u] += ((int64_t)w.tok * c.Hkv + h) * D + w.ch * 16;
     }
@@ -220,13 +222,17 @@ constexpr int MOVE_WARPS = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kvc::MOVE_WARPS * 32)
-    kv_commit_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, const int32_t* __restrict__ path,
-                     const int32_t* __restrict__ path_len, int32_t* pos_out, unsigned* err) {
+    kv_commit_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, const int32_t* path,
+                     const int32_t* path_len, int32_t* pos_out, unsigned* err) {
   using namespace kvc;
   constexpr int NODES = STRATA_TREE_MAX_NODES;
   constexpr int CPR = D / 16, HEADS = 256 / D;     // pieces per row; heads per warp
   constexpr int U = NODES / MOVE_WARPS;            // rows per warp
   __shared__ int64_t src[NODES], dst[NODES];
+  // the next kernel's CTAs wait until this one is done: let in early, they took 1.6
+  // us from 256 sequences' 64-node trees (8.7 us in a graph, this way 7.1; 7.5
+  // without programmatic launches)
+  stream_order_wait();
   const int b = blockIdx.y, th = threadIdx.x, warp = th / 32, lane = th % 32;
   const int pos = s.pos[b];
   int n = path_len[b];
@@ -287,23 +293,19 @@ cudaError_t launch_kv_append(const strata_kv_cache_t& c, const strata_kv_seqs_t&
                              const uint16_t* k, const uint16_t* v, int64_t stride, unsigned* err,
                              cudaStream_t stream) {
   if (c.D == 128)
-    kv_append_kernel<128><<<RowLanes<128>::ctas(c, s), kvc::THREADS, 0, stream>>>(c, s, k, v,
-                                                                                  stride, err);
-  else
-    kv_append_kernel<64><<<RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream>>>(c, s, k, v, stride,
-                                                                                err);
-  return cudaGetLastError();
+    return launch_in_order(kv_append_kernel<128>, RowLanes<128>::ctas(c, s), kvc::THREADS, 0,
+                           stream, 0, c, s, k, v, stride, err);
+  return launch_in_order(kv_append_kernel<64>, RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream, 0,
+                         c, s, k, v, stride, err);
 }
 
 cudaError_t launch_kv_read(const strata_kv_cache_t& c, const strata_kv_seqs_t& s, uint16_t* k_out,
                            uint16_t* v_out, unsigned* err, cudaStream_t stream) {
   if (c.D == 128)
-    kv_read_kernel<128><<<RowLanes<128>::ctas(c, s), kvc::THREADS, 0, stream>>>(c, s, k_out, v_out,
-                                                                                err);
-  else
-    kv_read_kernel<64><<<RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream>>>(c, s, k_out, v_out,
-                                                                              err);
-  return cudaGetLastError();
+    return launch_in_order(kv_read_kernel<128>, RowLanes<128>::ctas(c, s), kvc::THREADS, 0,
+                           stream, 0, c, s, k_out, v_out, err);
+  return launch_in_order(kv_read_kernel<64>, RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream, 0,
+                         c, s, k_out, v_out, err);
 }
 
 cudaError_t launch_kv_commit(const strata_kv_cache_t& c, const strata_kv_seqs_t& s,
@@ -312,22 +314,14 @@ cudaError_t launch_kv_commit(const strata_kv_cache_t& c, const strata_kv_seqs_t&
   const int heads = 256 / c.D, groups = (c.Hkv + heads - 1) / heads;
   // Two CTAs per SM, a cluster of 8 per sequence at most.  More of them wait
   // for a place and pay the chain position -> path -> page again: 256 paths at 8
-  // heads took 7.2 us with one CTA per sequence, 8.9 and 11.1 us with two and
-  // four; 32 paths 4.1 us with four.
+  // heads took 7.2 us with one CTA per sequence (7.0 with programmatic launches),
+  // 8.9 and 11.1 us with two and four; 32 paths 3.7 us with four.
   int ctas = 2 * sm_count() / s.B;
   ctas = ctas < 1 ? 1 : ctas > 8 ? 8 : ctas;
   if (ctas > groups) ctas = groups;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, s.B);
-  cfg.blockDim = dim3(kvc::MOVE_WARPS * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {(unsigned)ctas, 1, 1};
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, c.D == 128 ? kv_commit_kernel<128> : kv_commit_kernel<64>, c, s,
-                            path, path_len, pos_out, err);
+  return launch_in_order(c.D == 128 ? kv_commit_kernel<128> : kv_commit_kernel<64>, dim3(ctas, s.B),
+                         kvc::MOVE_WARPS * 32, 0, stream, (unsigned)ctas, c, s, path, path_len,
+                         pos_out, err);
 }
 
 }  // namespace strata

@@ -52,8 +52,8 @@
 // 24-node trees.
 //
 // Measured (D = 128, 4 KV heads, 32 query heads, one call, burst clocks): 32
-// sequences of 4 nodes behind up to 34,000 positions 108 us, 5.4 TB/s of the
-// cache's bytes (0.82 of the copy rate; the same with one node 97 us); one
+// sequences of 4 nodes behind up to 34,000 positions 107 us, 5.4 TB/s of the
+// cache's bytes (0.83 of the copy rate; the same with one node 97 us); one
 // sequence behind 34,000 22 us; one token behind 300 positions 11 us, of which 2 us
 // are the launch, 6 us the first tile's chain of dependent steps (lengths -> page
 // -> copy -> scores) and 2 us the join.  In a long line a tile takes a CTA
@@ -439,7 +439,6 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
   constexpr int W_TMA = NWG * 4, W_MMA = NWG * 4 + 1;
   const bool reporter = blockIdx.x == 0;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (th == 0) {
     for (int i = 0; i < KS; ++i) {
       mbar_init(&m.k_full[i], 1);
@@ -469,6 +468,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
     prefetch_tmap(&map_v);
   }
   if (warp == W_MMA) tmem_alloc(&m.tmem, F::TMEM_COLS);
+  stream_order_begin();
 
   // ---- the line: sequences in contiguous shares per thread, their lengths
   // scanned over the CTA
@@ -1196,58 +1196,20 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
 }
 
 // Joins the parts of the units that lie in more than one run, in run order:
-// one CTA of 8 warps per unit and 8 / WPR of its rows.  With few units
-// (WPR = 8) the CTA works out the unit's runs itself while the first kernel
-// is still busy; with many it reads them.
+// one CTA of 8 warps per unit and 8 / WPR of its rows.
 template <int D, int R, int WPR>
-__global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a, uint32_t ctas) {
+__global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a) {
   using namespace ta;
   constexpr int V = D / 32, U = 8;
   __shared__ float part_o[8][D], part_l[8], part_m[8];
-  __shared__ uint32_t scan[8][4];
+  stream_order_begin();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int unit = blockIdx.x;
   const int rb = unit % a.blocks, hk = unit / a.blocks % a.c.Hkv, b = unit / a.blocks / a.c.Hkv;
+  const Head hd = a.heads[unit];
   const TreeSeq t = tree_seq<R>(a, b, false);
-  Head hd = {0, 0};
-  if (WPR > 1) {
-    // tiles and units below sequence b, and of all sequences
-    uint32_t n[4] = {0, 0, 0, 0};
-    for (int i = threadIdx.x; i < a.s.B; i += 256) {
-      const TreeSeq x = tree_seq<R>(a, i, false);
-      const uint32_t units = x.units(a), tiles = units * x.tiles;
-      n[0] += tiles;
-      n[1] += units;
-      if (i < b) {
-        n[2] += tiles;
-        n[3] += units;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      n[k] = __reduce_add_sync(0xffffffffu, n[k]);
-      if (lane == 0) scan[warp][k] = n[k];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      n[k] = 0;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) n[k] += scan[w][k];
-    }
-    const Line line(n[0], n[1], ctas);
-    const uint32_t at = n[2] + line.cost * n[3] +
-                        (uint32_t)(hk * t.blocks + rb) * (t.tiles + line.cost) + line.cost;
-    if (rb < t.blocks) {
-      hd.run = (int)line.run_of(at);
-      hd.follow = (int)line.run_of(at + t.tiles - 1) - hd.run;
-    }
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // units of fewer nodes than N may not exist
-  if (rb >= t.blocks) return;
-  if (WPR == 1) hd = a.heads[unit];
-  if (hd.follow == 0) return;
+  // units of fewer nodes than N may not exist: their entry was not written
+  if (rb >= t.blocks || hd.follow == 0) return;
   const int r = blockIdx.y * (8 / WPR) + warp / WPR;
   const int flat = rb * R + r, node = flat / a.G, h = hk * a.G + flat % a.G;
   const int n = hd.follow + 1;
@@ -1357,23 +1319,14 @@ static cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const C
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   const int grid = tree_ctas(sm_count());
-  tree_attn_kernel<D, R><<<grid, F::THREADS, SMEM, stream>>>(mk, mv, a);
-  e = cudaGetLastError();
+  e = launch_in_order(tree_attn_kernel<D, R>, grid, F::THREADS, SMEM, stream, 0, mk, mv, a);
   if (e != cudaSuccess) return e;
   // many parts per unit: a row's parts over 8 warps; few: a row per warp
   const int units = a.s.B * a.c.Hkv * a.blocks;
   const bool wide = grid / units >= 4;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units, wide ? R : R / 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, tree_attn_combine_kernel<D, R, 8>, a, (uint32_t)grid)
-              : cudaLaunchKernelEx(&cfg, tree_attn_combine_kernel<D, R, 1>, a, (uint32_t)grid);
+  return launch_in_order(
+      wide ? tree_attn_combine_kernel<D, R, 8> : tree_attn_combine_kernel<D, R, 1>,
+      dim3(units, wide ? R : R / 8), 256, 0, stream, 0, a);
 }
 
 cudaError_t launch_tree_attn(const strata_kv_cache_t& c, const strata_kv_seqs_t& s,

@@ -19,7 +19,7 @@
 // Bound by the chain of passes of the sequence with the most rejections: a
 // pass over 100,003 tokens of p and q takes about 4.2 us (2.7 us the sums, of which
 // 0.8 us are the conversions to 64 bits, 0.9 us the cluster's barrier); a greedy
-// chain of 3 drafts at 32,000 tokens takes 6.3 us in all, 32 trees of 16 nodes at
+// chain of 3 drafts at 32,000 tokens takes 6.1 us in all, 32 trees of 16 nodes at
 // 100,003 tokens 27 us.  Holding a node's rows in shared memory between its
 // passes was no faster (29.7 against 31.4 us then, and slower without
 // rejections), nor were 256 or 1024 threads.
@@ -65,18 +65,24 @@ struct RestRow {
   __device__ __forceinline__ void load(int blk, float (&pv)[4], float (&qv)[4]) const {
     const int x0 = 4 * blk - shift;
     if (x0 >= 0 && x0 + 4 <= V) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p + x0));
-      pv[0] = a.x; pv[1] = a.y; pv[2] = a.z; pv[3] = a.w;
+      const uint4 a = ld_v4(p + x0);
+      pv[0] = __uint_as_float(a.x);
+      pv[1] = __uint_as_float(a.y);
+      pv[2] = __uint_as_float(a.z);
+      pv[3] = __uint_as_float(a.w);
       if (q) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(q + x0));
-        qv[0] = b.x; qv[1] = b.y; qv[2] = b.z; qv[3] = b.w;
+        const uint4 b = ld_v4(q + x0);
+        qv[0] = __uint_as_float(b.x);
+        qv[1] = __uint_as_float(b.y);
+        qv[2] = __uint_as_float(b.z);
+        qv[3] = __uint_as_float(b.w);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool in = x0 + j >= 0 && x0 + j < V;
-        pv[j] = in ? __ldg(p + x0 + j) : 0.f;
-        qv[j] = in && q ? __ldg(q + x0 + j) : 0.f;
+        pv[j] = in ? ld_f32(p + x0 + j) : 0.f;
+        qv[j] = in && q ? ld_f32(q + x0 + j) : 0.f;
       }
     }
   }
@@ -131,14 +137,13 @@ __device__ __forceinline__ double run_sum(const RestRow& row, int b0, int b1, in
 }
 
 __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREADS, 2)
-    verify_kernel(const int32_t* __restrict__ tokens, const int32_t* __restrict__ parent,
-                  const int32_t* __restrict__ count, const float* __restrict__ p,
-                  const float* __restrict__ q, const float* __restrict__ u_accept,
-                  const float* __restrict__ u_sample, int N, int V, int32_t* __restrict__ path,
-                  int32_t* __restrict__ path_len, int32_t* __restrict__ out_tokens,
-                  unsigned* err) {
+    verify_kernel(const int32_t* tokens, const int32_t* parent, const int32_t* count,
+                  const float* p, const float* q, const float* u_accept,
+                  const float* u_sample, int N, int V, int32_t* path, int32_t* path_len,
+                  int32_t* out_tokens, unsigned* err) {
   using namespace vd;
   extern __shared__ double block_sums[];     // of this CTA's blocks, for the next token
+  stream_order_begin();
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int b = blockIdx.x / CLUSTER;
@@ -181,8 +186,8 @@ __global__ void __cluster_dims__(vd::CLUSTER, 1, 1) __launch_bounds__(vd::THREAD
     float pv = 0.f, qv = 1.f;
     if (i > 0 && pa >= 0 && (unsigned)x < (unsigned)V) {
       const int64_t px = ((int64_t)b * N + pa) * V + x;
-      pv = __ldg(p + px);
-      if (q) qv = __ldg(q + px);
+      pv = ld_f32(p + px);
+      if (q) qv = ld_f32(q + px);
     }
     p_s[i] = pv;
     q_s[i] = qv;
@@ -371,9 +376,9 @@ cudaError_t launch_verify(const int32_t* tokens, const int32_t* parent, const in
         verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
   }
-  verify_kernel<<<B * vd::CLUSTER, vd::THREADS, bytes, stream>>>(
-      tokens, parent, count, p, q, u_accept, u_sample, N, V, path, path_len, out_tokens, err);
-  return cudaGetLastError();
+  return launch_in_order(verify_kernel, B * vd::CLUSTER, vd::THREADS, bytes, stream, 0, tokens,
+                         parent, count, p, q, u_accept, u_sample, N, V, path, path_len, out_tokens,
+                         err);
 }
 
 }  // namespace strata
