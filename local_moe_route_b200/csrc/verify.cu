@@ -369,11 +369,18 @@ cudaError_t launch_verify(const int32_t* tokens, const int32_t* parent, const in
                           const float* u_sample, int B, int N, int V, int32_t* path,
                           int32_t* path_len, int32_t* out_tokens, unsigned* err,
                           cudaStream_t stream) {
-  const int per = ((V + 3) / 4 + 1 + vd::CLUSTER * vd::WARPS - 1) / (vd::CLUSTER * vd::WARPS);
-  const size_t bytes = (size_t)per * vd::WARPS * sizeof(double);
-  if (bytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  auto sums_bytes = [](int v) {
+    const int per = ((v + 3) / 4 + 1 + vd::CLUSTER * vd::WARPS - 1) / (vd::CLUSTER * vd::WARPS);
+    return per * vd::WARPS * (int)sizeof(double);
+  };
+  const int bytes = sums_bytes(V);
+  // Asked for from well below 48 KB on, which the kernel's other shared memory
+  // counts towards, and always the most, whatever V is: another thread's call
+  // may set it between this and the launch.
+  if (bytes > 40 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sums_bytes(STRATA_VERIFY_MAX_VOCAB));
     if (e != cudaSuccess) return e;
   }
   return launch_in_order(verify_kernel, B * vd::CLUSTER, vd::THREADS, bytes, stream, 0, tokens,

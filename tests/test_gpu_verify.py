@@ -2,6 +2,8 @@
 numbers with one right answer, compared exactly, and a whole speculative step
 with all five entry points."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -74,6 +76,48 @@ def test_verify(V, kind, draft, dev):
     out = run(a, dev)
     assert_device_ok()
     check(a, out)
+
+
+@pytest.mark.parametrize("V", [180000, 181300, 190001, 196600, 230000, 800000])
+def test_verify_vocabularies_whose_sums_need_large_shared_memory(V, dev):
+    """Around the size from which a kernel's shared memory (the sums of four
+    probabilities and what is there for every V) has to be asked for."""
+    rng = np.random.default_rng(V)
+    a = make(rng, 1, 3, V, "star")
+    out = run(a, dev)
+    assert_device_ok()
+    check(a, out)
+
+
+def test_verify_from_two_threads_with_different_vocabularies(dev):
+    """Calls of two host threads, one with a far larger vocabulary: neither takes
+    away the shared memory the other's launch needs."""
+    jobs = []
+    for V in (210000, 790000):
+        a = make(np.random.default_rng(V), 1, 2, V, "chain")
+        jobs.append((a, [up(a[n], dev) for n in ("tokens", "p", "q", "u_accept", "u_sample")],
+                     [torch.zeros(s, dtype=torch.int32, device=dev) for s in ((1, 2), (1,), (1, 2))],
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    status = []
+
+    def work(job):
+        a, (tok, p, q, ua, us), out, stream = job
+        dims = sm.VerifyDims.of((1, 2, p.shape[2]))
+        for _ in range(1500):
+            status.append(sm.strata_verify_drafts(tok, None, None, p, q, ua, us, dims, *out,
+                                                  stream=stream))
+
+    threads = [threading.Thread(target=work, args=(job,)) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(status) == 3000 and set(status) == {sm.STRATA_OK}
+    assert_device_ok()
+    for a, _, out, _ in jobs:
+        check(a, out)
 
 
 def test_verify_sizes_counts_and_many_rejections(dev):
