@@ -113,6 +113,8 @@ STRATA_API strata_status_t strata_kv_read(strata_kv_cache_t cache, strata_kv_seq
  *            were; a node that sees no row gets zeros; may be q itself
  *            (q_stride = Hq * D)
  * Values at positions a node does not see, NaN among them, do not reach it.
+ * The sums over the positions hold 448 times the weights and V: with |V| up to
+ * 2^87 they stay finite at any length, up to 2^103 at 32,768 positions.
  * Scores, softmax and sums in fp32; for the product with V the weights of a tile
  * of 256 positions are rounded to 2^-9 of their value, or to 2^-17.8 of the
  * tile's largest weight (times the V scale of the row it belongs to, if that is

@@ -4,6 +4,9 @@ the call before) is complete when the call reads, and a call's results are compl
 when the next work reads them. The same steps with a synchronisation after
 everything are the reference; every result is the same bit for bit."""
 
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -194,3 +197,62 @@ def test_calls_of_two_streams_and_one_cache_at_once(D, dev):
     for job, w in zip(jobs, want):
         assert torch.equal(job[2], w)
     assert_device_ok()
+
+
+FIRST = """
+import torch
+import local_moe_route_b200 as sm
+dev = torch.device("cuda", 0)
+torch.manual_seed(1)
+i32 = dict(dtype=torch.int32, device=dev)
+B, N, Hkv, Hq, D, page, V = 2, 3, 2, 8, 128, 16, 200001
+c = sm.KvCache.empty(8, page, Hkv, D, dev)
+pos = torch.tensor([20, 9], **i32)
+s = sm.KvSeqs.of(torch.arange(8, **i32).view(2, 4), pos, N=N)
+back = sm.KvSeqs.of(torch.arange(8, **i32).view(2, 4), torch.zeros(2, **i32), N=24)
+k, v = (torch.randn(B, N, Hkv, D, device=dev).bfloat16() for _ in "kv")
+q = torch.randn(B, N, Hq, D, device=dev).bfloat16()
+p = torch.softmax(torch.randn(B, N, V, device=dev), -1)
+tok = p.argmax(-1).to(torch.int32).roll(1, 1).contiguous()
+ua, us = torch.full((B, N), 1e-9, device=dev), torch.full((B,), 0.5, device=dev)
+path, n, toks = torch.zeros(B, N, **i32), torch.zeros(B, **i32), torch.zeros(B, N, **i32)
+out, pos_out = torch.zeros_like(q), torch.zeros(B, **i32)
+kv = [torch.zeros(B, 24, Hkv, D, dtype=torch.bfloat16, device=dev) for _ in "kv"]
+ws = sm.tree_attention_workspace(c, s, Hq, dev)
+
+def step():
+    sm.check(sm.strata_kv_append(c, s, k, v))
+    sm.check(sm.strata_tree_attention(c, s, None, q, 0.0, out, ws))
+    sm.check(sm.strata_verify_drafts(tok, None, None, p, None, ua, us, (B, N, V), path, n, toks))
+    sm.check(sm.strata_kv_commit(c, s, path, n, pos_out))
+    sm.check(sm.strata_kv_read(c, back, *kv))
+
+def results():
+    torch.cuda.synchronize()
+    return [t.clone() for t in (out, path, n, toks, pos_out, *kv)]
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+got = results()
+for t in (out, path, n, toks, pos_out, *kv, *c.tensors):
+    t.zero_()
+step()
+want = results()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert bool((want[0] != 0).any()) and bool((want[2] > 0).all())
+sm.check(sm.strata_moe_device_status())
+print("same")
+"""
+
+
+def test_a_processs_first_calls_may_be_captured(dev):
+    """Nothing has to be called before a capture: a process whose first calls of
+    the library are captured gets what the same calls give outside a graph."""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr
