@@ -151,17 +151,26 @@ __global__ void __launch_bounds__(kvc::THREADS)
   }
 }
 
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&x)[8]) {   // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t dequantise2(uint32_t codes, float f) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
   const float2 y = __fmul2_rn(__half22float2(__half2(h)), make_float2(f, f));
   return pack_bf16x2(y.x, y.y);
 }
 
-// 34,000 positions at 4 heads (105 MB, two thirds of them written) take 22.6 us,
-// 4.7 TB/s; 8 values per lane with contiguous stores, or one or four steps in
-// flight instead of two, were no faster.
-template <int D>
-__global__ void __launch_bounds__(kvc::THREADS)
+// 34,000 positions at 4 heads (105 MB, two thirds of them written) take 19.7 us,
+// 5.3 TB/s.  The sixteen values of a lane leave in one store of 32 bytes (WIDE) where
+// the outputs start on such a boundary (every allocation of its own does): two of
+// 16 bytes, half a sector each, took 22.6 us.  Eight CTAs per SM (32 registers)
+// instead of five 19.7 for 20.6; one or four steps in flight instead of two 20.7
+// and 24.3, 128 or 512 threads 21.3 and 25.6.
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(kvc::THREADS, 8)
     kv_read_kernel(strata_kv_cache_t c, strata_kv_seqs_t s, uint16_t* k_out, uint16_t* v_out,
                    unsigned* err) {
   constexpr int U = 2;
@@ -204,8 +213,12 @@ __global__ void __launch_bounds__(kvc::THREADS)
         y[2 * i] = dequantise2(x[i] & 0xFFFFu, f);
         y[2 * i + 1] = dequantise2(x[i] >> 16, f);
       }
-      reinterpret_cast<uint4*>(out[u])[0] = make_uint4(y[0], y[1], y[2], y[3]);
-      reinterpret_cast<uint4*>(out[u])[1] = make_uint4(y[4], y[5], y[6], y[7]);
+      if (WIDE) {
+        st_v8(out[u], y);
+      } else {
+        reinterpret_cast<uint4*>(out[u])[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<uint4*>(out[u])[1] = make_uint4(y[4], y[5], y[6], y[7]);
+      }
     }
   }
 }
@@ -301,11 +314,15 @@ cudaError_t launch_kv_append(const strata_kv_cache_t& c, const strata_kv_seqs_t&
 
 cudaError_t launch_kv_read(const strata_kv_cache_t& c, const strata_kv_seqs_t& s, uint16_t* k_out,
                            uint16_t* v_out, unsigned* err, cudaStream_t stream) {
+  const bool wide =
+      ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   if (c.D == 128)
-    return launch_in_order(kv_read_kernel<128>, RowLanes<128>::ctas(c, s), kvc::THREADS, 0,
-                           stream, 0, c, s, k_out, v_out, err);
-  return launch_in_order(kv_read_kernel<64>, RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream, 0,
-                         c, s, k_out, v_out, err);
+    return launch_in_order(wide ? kv_read_kernel<128, true> : kv_read_kernel<128, false>,
+                           RowLanes<128>::ctas(c, s), kvc::THREADS, 0, stream, 0, c, s, k_out,
+                           v_out, err);
+  return launch_in_order(wide ? kv_read_kernel<64, true> : kv_read_kernel<64, false>,
+                         RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream, 0, c, s, k_out, v_out,
+                         err);
 }
 
 cudaError_t launch_kv_commit(const strata_kv_cache_t& c, const strata_kv_seqs_t& s,

@@ -166,6 +166,30 @@ def test_read_of_one_side_and_of_empty_rows(dev):
     assert np.all(got[0, 15, 1] == 0) and np.any(got[0, 15, 0] != 0)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("off_k,off_v", [(0, 0), (8, 0), (0, 8), (24, 40)])
+def test_read_to_outputs_on_16_byte_boundaries(D, off_k, off_v, dev):
+    """Outputs that start 16 bytes behind a 32-byte boundary, and what lies
+    around them is left alone."""
+    a = Setup(np.random.default_rng(17), dev, [3, 40, 0], [9, 20, 0], 20, 3, D, 32)
+    n = 3 * 20 * 3 * D
+    flat = [torch.full((n + 64,), 7.0, dtype=torch.bfloat16, device=dev) for _ in "kv"]
+    outs = [f[o:o + n].view(3, 20, 3, D) for f, o in zip(flat, (off_k, off_v))]
+    assert [o.data_ptr() % 32 for o in outs] == [2 * off_k % 32, 2 * off_v % 32]
+    plain = [torch.full((3, 20, 3, D), 7.0, dtype=torch.bfloat16, device=dev) for _ in "kv"]
+    sm.check(sm.strata_kv_read(a.c, a.s, *outs))
+    sm.check(sm.strata_kv_read(a.c, a.s, *plain))
+    assert_device_ok()
+    want = osp.read(a.cache, a.table, a.pos, a.count, 20)
+    for f, o, out, p, w in zip(flat, (off_k, off_v), outs, plain, want):
+        assert torch.equal(out.view(torch.int16), p.view(torch.int16))
+        got = bf16_to_f64(bf16_host(out))
+        for b, k in enumerate(a.count):
+            assert np.all(got[b, k:] == 7.0)
+            assert np.array_equal(got[b, :k], np.asarray(w, np.float64)[b, :k])
+        assert bool((f[:o] == 7.0).all()) and bool((f[o + n:] == 7.0).all())
+
+
 def test_bad_pages_and_ranges_are_reported_and_skipped(dev):
     rng = np.random.default_rng(8)
     a = Setup(rng, dev, [10, 0, 20, -1], [8, 4, 99, 2], 8, 2, 64, 16)
