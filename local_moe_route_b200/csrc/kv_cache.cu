@@ -77,8 +77,8 @@ __device__ __forceinline__ uint4 quantise16(const uint4& x0, const uint4& x1, in
 
 // How the lanes of a warp share the rows of the call.  D / 16 lanes take a row
 // (16 values each), so a warp takes RPS = 512 / D rows at a time.  A token's
-// 2 * Hkv rows (K of every head, then V of every head) go to one warp in steps of
-// RPS; when they are fewer than RPS, several tokens share the warp.
+// 2 * Hkv rows (K of every head, then V of every head) go to one warp or several in
+// steps of RPS; when they are fewer than RPS, several tokens share the warp.
 template <int D>
 struct RowLanes {
   static constexpr int LPR = D / 16, RPS = 32 / LPR;
@@ -95,9 +95,20 @@ struct RowLanes {
     const int64_t t = (int64_t)warp * tpw + mine;
     tok = mine < tpw && t < (int64_t)s.B * s.N ? (int)t : -1;
   }
-  static int ctas(const strata_kv_cache_t& c, const strata_kv_seqs_t& s) {
+  // CTAs for all tokens (x) and how many warps share a token's rows (y), each of
+  // which takes every y-th lot of `lot` steps: one lot per warp up to two CTAs per
+  // SM, two up to four CTAs per SM, four beyond.  Every warp pays the chain
+  // position -> page, every lot its loads.  Appending to 32 heads of D = 128 (16 lots),
+  // one warp per token -> this: 32 tokens 9.5 -> 2.1 us, 256 tokens 9.7 -> 2.9, 2048
+  // tokens 17.8 -> 10.7; 4 heads (2 lots), 32 tokens 2.5 -> 2.0, 24,576 tokens 14.3 and
+  // 18.5 with one lot per warp.  Reading 64 positions of 3 sequences at 32 heads 4.3 ->
+  // 2.6.
+  static dim3 grid(const strata_kv_cache_t& c, const strata_kv_seqs_t& s, int lot) {
     const int rows = 2 * c.Hkv, tpw = rows < RPS ? RPS / rows : 1;
-    return (int)(((int64_t)s.B * s.N + kvc::WARPS * tpw - 1) / (kvc::WARPS * tpw));
+    const int64_t x = ((int64_t)s.B * s.N + kvc::WARPS * tpw - 1) / (kvc::WARPS * tpw);
+    const int n = (rows + lot * RPS - 1) / (lot * RPS), sms = sm_count();
+    const int y = x * n <= 2 * sms ? n : x * ((n + 1) / 2) <= 4 * sms ? (n + 1) / 2 : (n + 3) / 4;
+    return dim3((unsigned)x, (unsigned)y);
   }
 };
 
@@ -116,7 +127,7 @@ __device__ __forceinline__ int64_t token_pos(const strata_kv_seqs_t& s, int tok,
 // Bound by its bytes once there are tens of thousands of rows, by the chain
 // position -> page -> row below; the rows' loads are in flight while the page is
 // looked up (their addresses do not depend on it).  Four 6144-token chunks (57 MB)
-// take 14.7 us, 3.9 TB/s; two steps in flight per warp 16.3 us (more registers,
+// take 14.3 us, 4.0 TB/s; two steps in flight per warp 16.3 us (more registers,
 // fewer warps), two tokens per warp 10 % more.
 template <int D>
 __global__ void __launch_bounds__(kvc::THREADS)
@@ -127,8 +138,9 @@ __global__ void __launch_bounds__(kvc::THREADS)
   int b = 0;
   const int64_t pos = token_pos(s, w.tok, &b, err);
   const int rows = 2 * c.Hkv;
-  int64_t row = -1;
-  for (int r0 = 0; r0 < rows; r0 += w.step) {
+  int row = -1;
+  const int first = blockIdx.y * w.step;
+  for (int r0 = first; r0 < rows; r0 += gridDim.y * w.step) {
     const int r = r0 + w.r;
     const bool is_v = r >= c.Hkv;
     const int h = is_v ? r - c.Hkv : r;
@@ -138,14 +150,14 @@ __global__ void __launch_bounds__(kvc::THREADS)
       x[0] = ld_v4(src);
       x[1] = ld_v4(src + 8);
     }
-    if (r0 == 0 && pos >= 0) {
-      row = row_of(c, s, b, pos);
+    if (r0 == first && pos >= 0) {
+      row = (int)row_of(c, s, b, pos);
       if (row < 0) atomicOr(err, kErrIndex);
     }
     int biased;
     const uint4 code = quantise16<D>(x[0], x[1], &biased);
     if (r >= rows || row < 0) continue;
-    const int64_t at = row + (int64_t)h * c.page;
+    const int64_t at = row + h * c.page;
     *reinterpret_cast<uint4*>((is_v ? c.v : c.k) + at * D + w.ch * 16) = code;
     if (w.ch == 0) (is_v ? c.v_exp : c.k_exp)[at] = (uint8_t)biased;
   }
@@ -163,8 +175,8 @@ __device__ __forceinline__ uint32_t dequantise2(uint32_t codes, float f) {
   return pack_bf16x2(y.x, y.y);
 }
 
-// 34,000 positions at 4 heads (105 MB, two thirds of them written) take 19.7 us,
-// 5.3 TB/s.  The sixteen values of a lane leave in one store of 32 bytes (WIDE) where
+// 34,000 positions at 4 heads (105 MB, two thirds of them written) take 19.1 us,
+// 5.5 TB/s.  The sixteen values of a lane leave in one store of 32 bytes (WIDE) where
 // the outputs start on such a boundary (every allocation of its own does): two of
 // 16 bytes, half a sector each, took 22.6 us.  Eight CTAs per SM (32 registers)
 // instead of five 19.7 for 20.6; one or four steps in flight instead of two 20.7
@@ -179,10 +191,10 @@ __global__ void __launch_bounds__(kvc::THREADS, 8)
   int b = 0;
   const int64_t pos = token_pos(s, w.tok, &b, err);
   if (pos < 0) return;
-  const int64_t row = row_of(c, s, b, pos);
+  const int row = (int)row_of(c, s, b, pos);
   if (row < 0) atomicOr(err, kErrIndex);
   const int rows = 2 * c.Hkv;
-  for (int r0 = 0; r0 < rows; r0 += U * w.step) {
+  for (int r0 = blockIdx.y * U * w.step; r0 < rows; r0 += gridDim.y * U * w.step) {
     uint4 code[U];
     int e[U];
     uint16_t* out[U];
@@ -195,7 +207,7 @@ __global__ void __launch_bounds__(kvc::THREADS, 8)
       code[u] = make_uint4(0, 0, 0, 0);
       e[u] = 0;
       if (out[u] && row >= 0) {
-        const int64_t at = row + (int64_t)h * c.page;
+        const int64_t at = row + h * c.page;
         e[u] = (is_v ? c.v_exp : c.k_exp)[at];
         code[u] = ld_v4((is_v ? c.v : c.k) + at * D + w.ch * 16);
       }
@@ -306,10 +318,10 @@ cudaError_t launch_kv_append(const strata_kv_cache_t& c, const strata_kv_seqs_t&
                              const uint16_t* k, const uint16_t* v, int64_t stride, unsigned* err,
                              cudaStream_t stream) {
   if (c.D == 128)
-    return launch_in_order(kv_append_kernel<128>, RowLanes<128>::ctas(c, s), kvc::THREADS, 0,
+    return launch_in_order(kv_append_kernel<128>, RowLanes<128>::grid(c, s, 1), kvc::THREADS, 0,
                            stream, 0, c, s, k, v, stride, err);
-  return launch_in_order(kv_append_kernel<64>, RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream, 0,
-                         c, s, k, v, stride, err);
+  return launch_in_order(kv_append_kernel<64>, RowLanes<64>::grid(c, s, 1), kvc::THREADS, 0, stream,
+                         0, c, s, k, v, stride, err);
 }
 
 cudaError_t launch_kv_read(const strata_kv_cache_t& c, const strata_kv_seqs_t& s, uint16_t* k_out,
@@ -318,11 +330,11 @@ cudaError_t launch_kv_read(const strata_kv_cache_t& c, const strata_kv_seqs_t& s
       ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   if (c.D == 128)
     return launch_in_order(wide ? kv_read_kernel<128, true> : kv_read_kernel<128, false>,
-                           RowLanes<128>::ctas(c, s), kvc::THREADS, 0, stream, 0, c, s, k_out,
-                           v_out, err);
+                           RowLanes<128>::grid(c, s, 2), kvc::THREADS, 0, stream, 0, c, s,
+                           k_out, v_out, err);
   return launch_in_order(wide ? kv_read_kernel<64, true> : kv_read_kernel<64, false>,
-                         RowLanes<64>::ctas(c, s), kvc::THREADS, 0, stream, 0, c, s, k_out, v_out,
-                         err);
+                         RowLanes<64>::grid(c, s, 2), kvc::THREADS, 0, stream, 0, c, s, k_out,
+                         v_out, err);
 }
 
 cudaError_t launch_kv_commit(const strata_kv_cache_t& c, const strata_kv_seqs_t& s,

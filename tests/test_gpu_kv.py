@@ -166,6 +166,25 @@ def test_read_of_one_side_and_of_empty_rows(dev):
     assert np.all(got[0, 15, 1] == 0) and np.any(got[0, 15, 0] != 0)
 
 
+@pytest.mark.parametrize("B,N,Hkv,D", [(3, 2, 32, 128), (2, 9, 33, 64), (2, 100, 31, 128),
+                                       (1, 700, 9, 128), (1, 640, 17, 64)])
+def test_append_and_read_of_many_heads(B, N, Hkv, D, dev):
+    """A token's rows over one warp, or over as many as there are steps, or between."""
+    rng = np.random.default_rng(Hkv)
+    a = Setup(rng, dev, rng.integers(0, 40, B), rng.integers(0, N + 1, B), N, Hkv, D, 32)
+    k, v = (bf16_bits(rng.standard_normal((B, N, Hkv, D)).astype(np.float32)) for _ in "kv")
+    sm.check(sm.strata_kv_append(a.c, a.s, up_bf16(k, dev), up_bf16(v, dev)))
+    out = [torch.full((B, N, Hkv, D), -7.0, dtype=torch.bfloat16, device=dev) for _ in "kv"]
+    sm.check(sm.strata_kv_read(a.c, a.s, *out))
+    assert_device_ok()
+    osp.append(a.cache, a.table, a.pos, a.count, k, v)
+    same_cache(a.held(), a.cache)
+    for o, r in zip(out, osp.read(a.cache, a.table, a.pos, a.count, N)):
+        o = bf16_to_f64(bf16_host(o))
+        for b, n in enumerate(a.count):
+            assert np.all(o[b, n:] == -7.0) and np.array_equal(o[b, :n], r[b, :n])
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("off_k,off_v", [(0, 0), (8, 0), (0, 8), (24, 40)])
 def test_read_to_outputs_on_16_byte_boundaries(D, off_k, off_v, dev):
