@@ -52,9 +52,9 @@
 // 24-node trees.
 //
 // Measured (D = 128, 4 KV heads, 32 query heads, one call, burst clocks): 32
-// sequences of 4 nodes behind up to 34,000 positions 107 us, 5.4 TB/s of the
-// cache's bytes (0.83 of the copy rate; the same with one node 97 us); one
-// sequence behind 34,000 22 us; one token behind 300 positions 11 us, of which 2 us
+// sequences of 4 nodes behind up to 34,000 positions 105 us, 5.5 TB/s of the
+// cache's bytes (0.84 of the copy rate; the same with one node 97 us); one
+// sequence behind 34,000 21 us; one token behind 300 positions 10 us, of which 2 us
 // are the launch, 6 us the first tile's chain of dependent steps (lengths -> page
 // -> copy -> scores) and 2 us the join.  In a long line a tile takes a CTA
 // 3.3 us, with two CTAs per SM near what its 66 KB take at the copy rate; D = 64
@@ -128,7 +128,7 @@ struct Misc {
   Unit unit[UNITS];
   uint32_t tmem;
   int abort;
-  int parent[UNITS][NODES];
+  unsigned long long sees[UNITS][R]; // nodes that a row sees
   int row[UNITS][R];                 // a row's node and query head: node * Hq + head
   int row_node[UNITS][R];
   uint2 scan[F::THREADS / 32];
@@ -138,7 +138,7 @@ struct Misc {
   alignas(16) float qf[R];                    // score factor of the row
   alignas(16) float wmax[F::NWG][4][C];       // per warp: largest score of the tile
   alignas(16) uint32_t wexp[F::NWG][4][C];    // per warp: largest visible V exponent
-  uint32_t wtop[F::NWG][4];
+  uint2 wtop[F::NWG][4];                      // the same over all rows: of positions, of nodes
   alignas(16) float mref[F::NWG][C], beta[F::NWG][C], alpha[F::NWG][C];
   alignas(16) float beta_o[F::NWG][2][C];
   alignas(16) float eh[F::NWG][C];            // a row's V exponent as a factor
@@ -407,6 +407,37 @@ __device__ __forceinline__ void split4(uint32_t h01, uint32_t h23, uint32_t* hi,
   }
 }
 
+// The nodes that `node` sees (itself and those above it, as bits), per lane, from
+// the parents of nodes lane and lane + 32 (-1: none; below the node itself): every
+// round doubles the number of generations a node knows of.  Followed one by one,
+// the parents of a chain of 64 nodes cost 3.2 of 18.7 us.
+__device__ __forceinline__ unsigned long long row_sees(int (&up)[2], int node, int lane) {
+  const uint32_t all = 0xffffffffu;
+  uint32_t low = 1u << lane, low2 = 0, high2 = 1u << lane;     // of nodes lane, lane + 32
+#pragma unroll 1
+  while (__any_sync(all, up[0] >= 0 || up[1] >= 0)) {
+    const uint32_t m0 = __shfl_sync(all, low, up[0]), m1 = __shfl_sync(all, low, up[1]);
+    const uint32_t n1 = __shfl_sync(all, low2, up[1]), h1 = __shfl_sync(all, high2, up[1]);
+    const int u0 = __shfl_sync(all, up[0], up[0]), u1 = __shfl_sync(all, up[0], up[1]);
+    const int v1 = __shfl_sync(all, up[1], up[1]);
+    if (up[0] >= 0) {
+      low |= m0;
+      up[0] = u0;
+    }
+    if (up[1] >= 32) {
+      low2 |= n1;
+      high2 |= h1;
+      up[1] = v1;
+    } else if (up[1] >= 0) {
+      low2 |= m1;
+      up[1] = u1;
+    }
+  }
+  const uint32_t a = __shfl_sync(all, low, node), b = __shfl_sync(all, low2, node),
+                 c = __shfl_sync(all, high2, node);
+  return node < 32 ? a : node < 64 ? (unsigned long long)c << 32 | b : 0ull;
+}
+
 // Waits (with a limit) for the copies in flight into a ring of N stages, of
 // which `n` uses were armed: shared memory must outlive them.
 template <int N>
@@ -606,6 +637,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
         return false;
       if (some) {
         const bool drafts = (unsigned)u.stop * TILE > (unsigned)u.pos;
+        static_assert(NODES == 64, "two nodes per lane");
         const int flat = u.rb * R + lane;              // R <= 32: a row per lane
         int node = flat / a.G;
         const int head = u.hk * a.G + flat - node * a.G, row_q = node * a.Hq + head;
@@ -631,14 +663,17 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
           bulk_load(smem + F::QR_OFF + lane * D * 2,
                     a.q + ((int64_t)u.b * a.s.N + node) * a.q_stride + (int64_t)head * D, D * 2,
                     &m.qr_full);
+        if (drafts) {
 #pragma unroll
-        for (int j = 0; j < NODES / 32; ++j) {
-          const int i = j * 32 + lane;
-          if (up[j] < -1 || up[j] >= i) {
-            if (i < u.count) atomicOr(a.err, kErrIndex);
-            up[j] = -1;
+          for (int j = 0; j < NODES / 32; ++j) {
+            const int i = j * 32 + lane;
+            if (up[j] < -1 || up[j] >= i) {
+              atomicOr(a.err, kErrIndex);
+              up[j] = -1;
+            }
           }
-          m.parent[us][i] = up[j];
+          const unsigned long long sees = row_sees(up, node, lane);
+          if (lane < R) m.sees[us][lane] = sees;
         }
       }
       __syncwarp();
@@ -868,7 +903,17 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
       if (u.last) break;
       const unsigned pos = (unsigned)u.pos;
       const bool drafts = (unsigned)u.stop * TILE > pos;     // the run reaches the tree
-      if (th < NODES) m.seen_by[th] = 0;
+      if (drafts) {
+        constexpr int NPW = NODES / (ALL / 32);          // nodes per warp
+        const unsigned long long sees = lane < R ? m.sees[us][lane] >> (warp * NPW) : 0;
+        uint32_t by = 0;
+#pragma unroll
+        for (int i = 0; i < NPW; ++i) {
+          const uint32_t b = __ballot_sync(0xffffffffu, (sees >> i) & 1);
+          if (lane == i) by = b;
+        }
+        if (lane < NPW) m.seen_by[warp * NPW + lane] = by;
+      }
       if (th == 0) m.nan_nodes = 0;
       ok = ta_wait(&m.qr_full, un & 1, abort_flag, a.err) && ok;
       constexpr int LPR = D / 8;             // lanes per row, 8 values each
@@ -912,12 +957,6 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
       fence_proxy_async_smem();
       mbar_arrive(&m.q_full);
       dead = named_barrier_or(1, ALL, !ok);
-      if (!dead && drafts) {
-        if (th < R)
-          for (int j = min(m.row_node[us][th], NODES - 1); j >= 0; j = m.parent[us][j])
-            atomicOr(&m.seen_by[j], 1u << th);
-        named_barrier_sync(1, ALL);
-      }
       if (th == 0) mbar_arrive(&m.qr_empty);
 
       float m_run = -INFINITY;               // of column lt, in threads lt < C
@@ -984,29 +1023,41 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
                   make_float4(w[c], w[c + 1], w[c + 2], w[c + 3]);
           }
         }
-        if (tree) {
-          // the largest V exponent among what a row sees: one per row here
-#pragma unroll 4
+        {
+          // the largest V exponent, of positions that every row sees and of nodes
+          const unsigned t0 = (unsigned)tile * TILE + lt, t1 = t0 + SUB;
+          const uint32_t e0 = vis[0] ? ve[0] : 0u, e1 = vis[1] ? ve[1] : 0u;
+          uint2 w;
+          w.x = __reduce_max_sync(0xffffffffu, max(t0 < pos ? e0 : 0u, t1 < pos ? e1 : 0u));
+          w.y = tree ? __reduce_max_sync(0xffffffffu, max(t0 < pos ? 0u : e0, t1 < pos ? 0u : e1))
+                     : 0u;
+          if (lane == 0) m.wtop[wg][wq] = w;
+        }
+        named_barrier_sync(bar_wg, 128);
+        uint32_t etop = 0, enode = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          etop = max(etop, m.wtop[wg][i].x);
+          enode = max(enode, m.wtop[wg][i].y);
+        }
+        // a node with a larger one than those: one per row, of what it sees (always so:
+        // one sequence behind 34,000 positions 22.1 for 21.2 us)
+        const bool per_row = enode > etop;
+        if (per_row) {
+#pragma unroll 1
           for (int c = 0; c < C; ++c) {
             const uint32_t w = __reduce_max_sync(
                 0xffffffffu, max((vis[0] >> c) & 1 ? ve[0] : 0u, (vis[1] >> c) & 1 ? ve[1] : 0u));
             if (lane == 0) m.wexp[wg][wq][c] = w;
           }
-        } else {
-          const uint32_t w =
-              __reduce_max_sync(0xffffffffu, max(vis[0] ? ve[0] : 0u, vis[1] ? ve[1] : 0u));
-          if (lane == 0) m.wtop[wg][wq] = w;
+          named_barrier_sync(bar_wg, 128);
         }
-        named_barrier_sync(bar_wg, 128);
-        const uint32_t etop = tree ? 0u
-                                   : max(max(m.wtop[wg][0], m.wtop[wg][1]),
-                                         max(m.wtop[wg][2], m.wtop[wg][3]));
         bool moved = false;
         if (lt < C) {
           const float top = fmaxf(fmaxf(m.wmax[wg][0][lt], m.wmax[wg][1][lt]),
                                   fmaxf(m.wmax[wg][2][lt], m.wmax[wg][3][lt]));
           uint32_t ex = etop;
-          if (tree)
+          if (per_row)
             ex = max(max(m.wexp[wg][0][lt], m.wexp[wg][1][lt]),
                      max(m.wexp[wg][2][lt], m.wexp[wg][3][lt]));
           // 2^(127 - ex); 2^-127 is subnormal
@@ -1067,7 +1118,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
         for (int h = 0; h < 2; ++h) {
           // 2^(ev - E of the row); above 1 only where the weight is 0
           const float f = __uint_as_float(ve[h] << 23);
-          if (tree) {
+          if (per_row) {
 #pragma unroll
             for (int c = 0; c < C; ++c) s[h][c] *= fminf(f * m.eh[wg][c], 1.f);
             vf[h] = WSCALE;
@@ -1102,14 +1153,17 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
             ok = ta_wait(&m.v_full[j % VS], (j / VS) & 1, abort_flag, a.err) && ok;
             const unsigned t = (unsigned)tile * TILE + h * SUB + lt;
             uint4* vr = reinterpret_cast<uint4*>(sV + (j % VS) * F::KV_BYTES + lt * D);
+            // eight lanes' 16-byte pieces lie in different banks (one token behind 300
+            // positions 10.2 us; 10.8 with all lanes' pieces in one)
+            const int rot = D == 128 ? lane : lane / 2;
             if (t >= end || e[h * SUB] == 0 || e[TILE + h * SUB] == 0) {
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i) vr[i] = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < D / 16; ++i) vr[(i + rot) % (D / 16)] = make_uint4(0, 0, 0, 0);
             } else if (t >= pos) {
               uint32_t any = 0;        // a byte 0x7F without its sign carries into bit 7
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
-                const uint4 x = vr[i];
+                const uint4 x = vr[(i + rot) % (D / 16)];
                 any |= ((x.x & 0x7F7F7F7Fu) + 0x01010101u) | ((x.y & 0x7F7F7F7Fu) + 0x01010101u) |
                        ((x.z & 0x7F7F7F7Fu) + 0x01010101u) | ((x.w & 0x7F7F7F7Fu) + 0x01010101u);
               }
