@@ -68,6 +68,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "kv.h"
+#include "tree_parts.h"
 
 namespace strata {
 
@@ -75,7 +76,6 @@ namespace ta {
 constexpr int SUB = 128;                    // positions per MMA tile
 constexpr int TILE = 2 * SUB;               // positions per softmax step
 constexpr int NODES = STRATA_TREE_MAX_NODES;
-constexpr int MAX_CTAS = 148 * 2;           // CTAs the workspace has room for
 constexpr float WSCALE = 448.f;             // weights are scaled to e4m3's largest value
 // What a unit costs besides its tiles (its query rows, the tree's masks, its
 // results), in tiles: units take that much more of the line.  On short lines
@@ -144,13 +144,6 @@ struct Misc {
   alignas(16) float eh[F::NWG][C];            // a row's V exponent as a factor
   alignas(16) float lsum[F::NWG][4][C];       // per warp: sums of the weights
   alignas(16) float inv[R];                   // 1 / (sum * WSCALE)
-};
-
-// A run's first unit may have begun in an earlier run: slot 0; its last may go
-// on in the next: slot 1.  Per unit: the run that begins it, and how many
-// runs after that one go on with it.
-struct Head {
-  int run, follow;
 };
 
 __host__ __device__ constexpr size_t slot_floats(int R, int D) { return (size_t)R * (D + 2); }
@@ -1264,11 +1257,13 @@ __global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a
   const TreeSeq t = tree_seq<R>(a, b, false);
   // units of fewer nodes than N may not exist: their entry was not written
   if (rb >= t.blocks || hd.follow == 0) return;
+  if (!parts_within(hd)) {         // not written: a wait gave up before this unit
+    if (threadIdx.x == 0) atomicOr(a.err, kErrIndex);
+    return;
+  }
   const int r = blockIdx.y * (8 / WPR) + warp / WPR;
   const int flat = rb * R + r, node = flat / a.G, h = hk * a.G + flat % a.G;
   const int n = hd.follow + 1;
-  // part i: slot 1 of the first run, then slot 0 of the following ones
-  const float* base = a.parts + (size_t)2 * hd.run * slot_floats(R, D);
   float o[V], sum = 0.f, top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < V; ++j) o[j] = 0.f;
@@ -1280,7 +1275,7 @@ __global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a
       const int i = i0 + u * WPR;
       ml[u] = make_float2(-INFINITY, 0.f);
       if (i >= n) continue;
-      const float* p = base + (size_t)(2 * i + (i == 0)) * slot_floats(R, D);
+      const float* p = a.parts + (size_t)part_slot(hd, i) * slot_floats(R, D);
       ml[u] = *reinterpret_cast<const float2*>(p + R * D + 2 * r);
       if constexpr (V == 4) {
         const float4 x = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
