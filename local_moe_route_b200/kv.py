@@ -87,6 +87,17 @@ def _rows(t: Any, dev: int, B: int, N: int, heads: int, D: int):
     return t.data_ptr(), step
 
 
+def _step(given: int, own: int, dense: int, *rows: Any) -> int:
+    """The token stride of a call: that of tensors that are parts of wider rows, or the
+    one given with raw pointers.  Beside a dense tensor any other than its own would
+    lead past its end."""
+    if own:
+        return own
+    if given and given != dense and any(t is not None and t.__class__ is not int for t in rows):
+        raise _Refused
+    return given
+
+
 def _on(stream: Any, dev: int) -> Optional[int]:
     """The stream's handle; None = the current stream of the current device."""
     return _raw_stream(dev) if stream is None and dev >= 0 else _stream(stream)
@@ -184,17 +195,19 @@ def _lib() -> ctypes.CDLL:
 
 def strata_kv_append(cache: KvCache, seqs: KvSeqs, k, v, stride: int = 0, stream=None) -> int:
     """k, v [B][N][Hkv][D] bf16; tensors may be parts of wider rows (their token
-    stride is taken from them, `stride` is for raw pointers)."""
+    stride is taken from them, `stride` is for raw pointers: beside dense tensors another
+    than theirs is refused)."""
     dev = _device()
     try:
         _here(dev, cache, seqs)
         kp, ks = _rows(k, dev, seqs.B, seqs.N, cache.Hkv, cache.D)
         vp, vs = _rows(v, dev, seqs.B, seqs.N, cache.Hkv, cache.D)
+        if ks != vs:
+            raise _Refused
+        step = _step(stride, ks, cache.Hkv * cache.D, k, v)
     except _Refused:
         return STRATA_ERR_INVALID_ARG
-    if ks != vs:
-        return STRATA_ERR_INVALID_ARG
-    return (_bound or _lib()).strata_kv_append(cache, seqs, kp, vp, ks or stride, _on(stream, dev))
+    return (_bound or _lib()).strata_kv_append(cache, seqs, kp, vp, step, _on(stream, dev))
 
 
 def strata_kv_read(cache: KvCache, seqs: KvSeqs, k_out, v_out, stream=None) -> int:
@@ -236,7 +249,8 @@ def strata_tree_attention(cache: KvCache, seqs: KvSeqs, parent, q, scale, out, w
                           ws_bytes: Optional[int] = None, Hq: Optional[int] = None,
                           q_stride: int = 0, stream=None) -> int:
     """q, out [B][N][Hq][D] bf16, parent [B][N] int32 or None; a q tensor may be a
-    part of wider rows.  Hq and q_stride are for raw pointers."""
+    part of wider rows.  Hq and q_stride are for raw pointers; beside a dense q tensor
+    another q_stride than its own is refused."""
     dev = _device()
     B, N, D = seqs.B, seqs.N, cache.D
     try:
@@ -245,12 +259,13 @@ def strata_tree_attention(cache: KvCache, seqs: KvSeqs, parent, q, scale, out, w
             Hq = q.shape[2] if q.dim() == 4 else 0
         heads = int(Hq or 0)
         qp, qs = _rows(q, dev, B, N, heads, D)
+        step = _step(q_stride, qs, heads * D, q)
         op, pp = _dev(out, _bf16, dev, B * N * heads * D), _dev(parent, _i32, dev, B * N)
         wp = _dev(ws, _u8, dev)
     except _Refused:
         return STRATA_ERR_INVALID_ARG
     return (_bound or _lib()).strata_tree_attention(
-        cache, seqs, pp, qp, qs or q_stride, heads, scale, op, wp,
+        cache, seqs, pp, qp, step, heads, scale, op, wp,
         _nbytes(ws) if ws_bytes is None else ws_bytes, _on(stream, dev))
 
 
