@@ -98,6 +98,14 @@ def _step(given: int, own: int, dense: int, *rows: Any) -> int:
     return given
 
 
+def _ws_bytes(ws: Any, given: Optional[int]) -> int:
+    """Size of the workspace: what is given with a raw pointer, and no more than a
+    tensor has."""
+    if given is None:
+        return _nbytes(ws)
+    return int(given) if ws is None or ws.__class__ is int else min(int(given), _nbytes(ws))
+
+
 def _on(stream: Any, dev: int) -> Optional[int]:
     """The stream's handle; None = the current stream of the current device."""
     return _raw_stream(dev) if stream is None and dev >= 0 else _stream(stream)
@@ -266,7 +274,7 @@ def strata_tree_attention(cache: KvCache, seqs: KvSeqs, parent, q, scale, out, w
         return STRATA_ERR_INVALID_ARG
     return (_bound or _lib()).strata_tree_attention(
         cache, seqs, pp, qp, step, heads, scale, op, wp,
-        _nbytes(ws) if ws_bytes is None else ws_bytes, _on(stream, dev))
+        _ws_bytes(ws, ws_bytes), _on(stream, dev))
 
 
 def strata_verify_drafts(tokens, parent, count, p, q, u_accept, u_sample, dims, path, path_len,

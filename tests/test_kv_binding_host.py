@@ -113,3 +113,12 @@ def test_a_query_stride_beside_a_dense_tensor_is_refused_unless_it_is_its_own(li
         assert library.calls.pop()[1][4:6] == (wide, HQ)
         assert attend(FAKE, Hq=HQ, q_stride=stride) == OK
         assert library.calls.pop()[1][4:6] == (stride, HQ)
+
+
+def test_a_workspace_tensor_counts_as_what_it_has(library):
+    ws = Rows((4096,), torch.uint8)
+    for given, got in ((None, 4096), (4096, 4096), (100, 100), (4097, 4096), (1 << 40, 4096)):
+        assert attend(bf16(HQ), ws=ws, ws_bytes=given) == OK
+        assert library.calls.pop()[1][9] == got
+    assert attend(bf16(HQ), ws=FAKE, ws_bytes=1 << 30) == OK
+    assert library.calls.pop()[1][9] == 1 << 30
