@@ -103,7 +103,8 @@ def _ws_bytes(ws: Any, given: Optional[int]) -> int:
     tensor has."""
     if given is None:
         return _nbytes(ws)
-    return int(given) if ws is None or ws.__class__ is int else min(int(given), _nbytes(ws))
+    n = max(int(given), 0)               # (it travels as a size without a sign)
+    return n if ws is None or ws.__class__ is int else min(n, _nbytes(ws))
 
 
 def _on(stream: Any, dev: int) -> Optional[int]:

@@ -122,3 +122,10 @@ def test_a_workspace_tensor_counts_as_what_it_has(library):
         assert library.calls.pop()[1][9] == got
     assert attend(bf16(HQ), ws=FAKE, ws_bytes=1 << 30) == OK
     assert library.calls.pop()[1][9] == 1 << 30
+
+
+def test_a_negative_workspace_size_is_none_at_all(library):
+    for ws in (Rows((4096,), torch.uint8), FAKE):
+        for given in (-1, -4096, -(1 << 40)):
+            assert attend(bf16(HQ), ws=ws, ws_bytes=given) == OK
+            assert library.calls.pop()[1][9] == 0
