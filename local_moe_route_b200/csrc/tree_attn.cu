@@ -1210,7 +1210,8 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
           const int r = wg * C + lt;
           float sum = (m.lsum[wg][0][lt] + m.lsum[wg][1][lt]) +
                       (m.lsum[wg][2][lt] + m.lsum[wg][3][lt]);
-          if (m.nan_row[r]) sum = __uint_as_float(0x7FC00000u);
+          // (its scores are 0: without a position it sees nothing was added)
+          if (m.nan_row[r] && sum != 0.f) sum = __uint_as_float(0x7FC00000u);
           m.inv[r] = sum == 0.f ? 0.f : 1.f / (sum * WSCALE);
           if (!whole) {
             float* part =
