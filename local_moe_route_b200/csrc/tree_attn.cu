@@ -24,13 +24,17 @@
 // added in fp32 registers.
 //
 // A position's K exponent multiplies its scores, one factor per thread,
-// because a thread is a position there.  Its V exponent goes into the weight:
-// P = p * 2^(ev - E) * 448 with E the largest V exponent of the tile, and the
-// tile's O is added to the running sum as O * 2^E.  A tile's weights
-// are scaled to its own maximum, not to the running one, since e4m3 reaches
-// only 2^-9 (2^-17.8 of the tile's largest weight): positions of a tile far
-// below an earlier tile's maximum keep their precision.  References are
-// integers (log2 domain), so rescaling is an exponent addition.
+// because a thread is a position there.  Its V exponent goes into the weight,
+//   P = 2^(s + ev - r) * 448,   r = ceil(max (s + ev)) over what the row sees,
+// and the tile's O is added to the running sum as O * 2^r.  e4m3 reaches only
+// 2^-9 (2^-17.8 of the tile's largest weight), so what is scaled to that range is what
+// a position adds to the output, score and V scale together, per row and tile: a
+// large V that a row gives no weight to, or that another node sees, takes nothing
+// from the others, and positions of a tile far below an earlier tile's maximum keep
+// their precision.  The sum of the softmax comes from s alone, scaled to the same
+// r less the tile's largest exponent where its exponents lie close together, to its
+// own maximum (a third barrier) where they do not, e.g. beside a V row of zeros.
+// References are integers (log2 domain), so rescaling is an exponent addition.
 //
 // Work: the tiles (256 positions) of all (sequence, KV head, block of R rows)
 // units in one line, cut into equal runs, one per CTA, whatever the lengths are.
@@ -77,6 +81,9 @@ constexpr int SUB = 128;                    // positions per MMA tile
 constexpr int TILE = 2 * SUB;               // positions per softmax step
 constexpr int NODES = STRATA_TREE_MAX_NODES;
 constexpr float WSCALE = 448.f;             // weights are scaled to e4m3's largest value
+// V exponents of a tile that lie no further apart share one reference for the scores
+// and the weights (the sums then hold up to 2^SPREAD times the weights).
+constexpr int SPREAD = 30;
 // What a unit costs besides its tiles (its query rows, the tree's masks, its
 // results), in tiles: units take that much more of the line.  On short lines
 // the number of tiles per CTA counts, not their even cost.
@@ -136,12 +143,12 @@ struct Misc {
   int start_b;
   int nan_row[R];
   alignas(16) float qf[R];                    // score factor of the row
-  alignas(16) float wmax[F::NWG][4][C];       // per warp: largest score of the tile
-  alignas(16) uint32_t wexp[F::NWG][4][C];    // per warp: largest visible V exponent
-  uint2 wtop[F::NWG][4];                      // the same over all rows: of positions, of nodes
+  // per warp: largest score plus V exponent of the tile; largest score
+  alignas(16) float wmax[F::NWG][4][C], wscore[F::NWG][4][C];
+  uint2 wexp[F::NWG][4];      // per warp: largest V exponent that a row sees; 255 - the smallest
   alignas(16) float mref[F::NWG][C], beta[F::NWG][C], alpha[F::NWG][C];
   alignas(16) float beta_o[F::NWG][2][C];
-  alignas(16) float eh[F::NWG][C];            // a row's V exponent as a factor
+  alignas(16) float eh[F::NWG][C];            // per row: 2^-(the scale of its weights)
   alignas(16) float lsum[F::NWG][4][C];       // per warp: sums of the weights
   alignas(16) float inv[R];                   // 1 / (sum * WSCALE)
 };
@@ -1005,43 +1012,45 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
               if (!((vis[h] >> c) & 1)) s[h][c] = -INFINITY;
           }
         }
+        const float ev[2] = {(float)((int)ve[0] - 127), (float)((int)ve[1] - 127)};
         {
+          const f32x2 e0 = pair(ev[0], ev[0]), e1 = pair(ev[1], ev[1]);
           float w[C];
 #pragma unroll
-          for (int c = 0; c < C; ++c) w[c] = warp_max(fmaxf(s[0][c], s[1][c]));
+          for (int c = 0; c < C; c += 2) {
+            float x0, x1, y0, y1;
+            unpair(add2(pair(s[0][c], s[0][c + 1]), e0), x0, x1);
+            unpair(add2(pair(s[1][c], s[1][c + 1]), e1), y0, y1);
+            w[c] = warp_max(fmaxf(x0, y0));
+            w[c + 1] = warp_max(fmaxf(x1, y1));
+          }
           if (lane == 0) {
 #pragma unroll
             for (int c = 0; c < C; c += 4)
               *reinterpret_cast<float4*>(&m.wmax[wg][wq][c]) =
                   make_float4(w[c], w[c + 1], w[c + 2], w[c + 3]);
           }
-        }
-        {
-          // the largest V exponent, of positions that every row sees and of nodes
-          const unsigned t0 = (unsigned)tile * TILE + lt, t1 = t0 + SUB;
-          const uint32_t e0 = vis[0] ? ve[0] : 0u, e1 = vis[1] ? ve[1] : 0u;
-          uint2 w;
-          w.x = __reduce_max_sync(0xffffffffu, max(t0 < pos ? e0 : 0u, t1 < pos ? e1 : 0u));
-          w.y = tree ? __reduce_max_sync(0xffffffffu, max(t0 < pos ? 0u : e0, t1 < pos ? 0u : e1))
-                     : 0u;
-          if (lane == 0) m.wtop[wg][wq] = w;
+          uint2 e;
+          e.x = __reduce_max_sync(0xffffffffu, max(vis[0] ? ve[0] : 0u, vis[1] ? ve[1] : 0u));
+          e.y = __reduce_max_sync(0xffffffffu,
+                                  max(vis[0] ? 255u - ve[0] : 0u, vis[1] ? 255u - ve[1] : 0u));
+          if (lane == 0) m.wexp[wg][wq] = e;
         }
         named_barrier_sync(bar_wg, 128);
-        uint32_t etop = 0, enode = 0;
+        int etop = 0, elow = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          etop = max(etop, m.wtop[wg][i].x);
-          enode = max(enode, m.wtop[wg][i].y);
+          etop = max(etop, (int)m.wexp[wg][i].x);
+          elow = max(elow, (int)m.wexp[wg][i].y);
         }
-        // a node with a larger one than those: one per row, of what it sees (always so:
-        // one sequence behind 34,000 positions 22.1 for 21.2 us)
-        const bool per_row = enode > etop;
+        elow = 255 - elow;
+        // Far apart, and the scores need a maximum of their own
+        const bool per_row = etop - elow > SPREAD;
         if (per_row) {
-#pragma unroll 1
+#pragma unroll
           for (int c = 0; c < C; ++c) {
-            const uint32_t w = __reduce_max_sync(
-                0xffffffffu, max((vis[0] >> c) & 1 ? ve[0] : 0u, (vis[1] >> c) & 1 ? ve[1] : 0u));
-            if (lane == 0) m.wexp[wg][wq][c] = w;
+            const float w = warp_max(fmaxf(s[0][c], s[1][c]));
+            if (lane == 0) m.wscore[wg][wq][c] = w;
           }
           named_barrier_sync(bar_wg, 128);
         }
@@ -1049,14 +1058,19 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
         if (lt < C) {
           const float top = fmaxf(fmaxf(m.wmax[wg][0][lt], m.wmax[wg][1][lt]),
                                   fmaxf(m.wmax[wg][2][lt], m.wmax[wg][3][lt]));
-          uint32_t ex = etop;
-          if (per_row)
-            ex = max(max(m.wexp[wg][0][lt], m.wexp[wg][1][lt]),
-                     max(m.wexp[wg][2][lt], m.wexp[wg][3][lt]));
-          // 2^(127 - ex); 2^-127 is subnormal
-          m.eh[wg][lt] = ex < 254u ? __uint_as_float((254u - ex) << 23) : __uint_as_float(1u << 22);
+          // the reference of the row's scores, and of its weights above that
+          float ref = ceilf(top) - (float)(etop - 127);
+          int lift = etop - 127;
+          if (per_row) {
+            ref = ceilf(fmaxf(fmaxf(m.wscore[wg][0][lt], m.wscore[wg][1][lt]),
+                              fmaxf(m.wscore[wg][2][lt], m.wscore[wg][3][lt])));
+            lift = min(max((int)(ceilf(top) - ref), -127), 127);
+          }
+          // 2^-lift; 2^-127 is subnormal
+          m.eh[wg][lt] = lift < 127 ? __uint_as_float((uint32_t)(127 - lift) << 23)
+                                    : __uint_as_float(1u << 22);
           // a tile without a visible position changes nothing
-          const float ref = top == -INFINITY ? (m_run == -INFINITY ? 0.f : m_run) : ceilf(top);
+          if (top == -INFINITY) ref = m_run == -INFINITY ? 0.f : m_run;
           const float now = top == -INFINITY ? m_run : fmaxf(m_run, ref);
           float al = 1.f;
           if (now != m_run) {
@@ -1068,7 +1082,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
           m.mref[wg][lt] = -ref;
           m.alpha[wg][lt] = al;
           m.beta[wg][lt] = pow2i(d);
-          m.beta_o[wg][g & 1][lt] = pow2i(d + (int)ex - 127);
+          m.beta_o[wg][g & 1][lt] = pow2i(d + lift);
         }
         // (the references, and whether any moved or a wait gave up)
         const bool rescale = named_barrier_or(bar_wg, 128, moved || !ok);
@@ -1109,11 +1123,13 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
         float vf[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          // 2^(ev - E of the row); above 1 only where the weight is 0
+          // 2^(ev - lift).  Beyond the bounds only where the weight is 0: in the common
+          // case lift is the largest exponent, else weight and factor have a product
+          // of 1 at most, and the weight is 2^-126 at least
           const float f = __uint_as_float(ve[h] << 23);
           if (per_row) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) s[h][c] *= fminf(f * m.eh[wg][c], 1.f);
+            for (int c = 0; c < C; ++c) s[h][c] *= fminf(f * m.eh[wg][c], 0x1p126f);
             vf[h] = WSCALE;
           } else {
             vf[h] = fminf(f * m.eh[wg][0], 1.f) * WSCALE;
