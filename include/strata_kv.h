@@ -115,7 +115,8 @@ STRATA_API strata_status_t strata_kv_read(strata_kv_cache_t cache, strata_kv_seq
  * Values at positions a node does not see, NaN among them, do not reach it.
  * The sums over the positions hold 448 times the weights and V: with |V| up to
  * 2^87 they stay finite at any length, up to 2^103 at 32,768 positions.
- * Scores, softmax and sums in fp32; for the product with V what a position adds to
+ * Scores, softmax and sums in fp32 (values of q below 2^-13.8 of their row's largest
+ * are rounded to 2^-21.8 of it, all others taken as they are); for the product with V what a position adds to
  * a row (its weight times 2^(v_exp - 127)) is rounded to 2^-9 of its value, or to
  * 2^-17.8 of the row's largest in the same tile of 256 positions where that is
  * more: a large V without weight takes nothing from the others.

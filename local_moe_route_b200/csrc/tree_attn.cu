@@ -14,8 +14,10 @@
 //   S^T [128 positions][2R] = K tile [128][D] . [q_hi ; q_lo]^T
 //   O^T [D][2R]             = V tile^T [D][128] . [P_hi | P_lo]
 // A bf16 q (8 significant bits) times a power of two is the sum of two e4m3
-// values (4 bits each), so the scores are sums of exact products: the low
-// part is exact down to 2^-17 of the row's largest value.  The weights are
+// values (4 bits each), so the scores are sums of exact products.  The high part
+// leaves 16 of 448 at most, so the low part is held times 16: together they are
+// exact for values of q above 2^-13.8 of the row's largest and off by 2^-21.8 of
+// that at most below (2^-9.8 and 2^-17.8 with both parts on one scale).  The weights are
 // split the same way: p (fp32) is rounded to fp16 (2^-11), to e4m3, and
 // the remainder to e4m3 again, 2^-9 of the value in all.  Against one bf16
 // rounding of p (2^-8) that is half the error, and the tensor pipe never
@@ -81,6 +83,7 @@ constexpr int SUB = 128;                    // positions per MMA tile
 constexpr int TILE = 2 * SUB;               // positions per softmax step
 constexpr int NODES = STRATA_TREE_MAX_NODES;
 constexpr float WSCALE = 448.f;             // weights are scaled to e4m3's largest value
+constexpr float QLO = 16.f;                 // the low parts of q are held times this
 // V exponents of a tile that lie no further apart share one reference for the scores
 // and the weights (the sums then hold up to 2^SPREAD times the weights).
 constexpr int SPREAD = 30;
@@ -943,7 +946,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
           const __nv_fp8x2_storage_t c8 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
           const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c8, __NV_E4M3)));
           const __nv_fp8x2_storage_t r8 = __nv_cvt_float2_to_fp8x2(
-              make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
+              make_float2(QLO * (y.x - back.x), QLO * (y.y - back.y)), __NV_SATFINITE, __NV_E4M3);
           hi[i / 2] |= (uint32_t)c8 << (16 * (i & 1));
           lo[i / 2] |= (uint32_t)r8 << (16 * (i & 1));
         }
@@ -986,6 +989,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
         ok = ta_wait(&m.s_full, g & 1, abort_flag, a.err) && ok;
         tc_fence_after();
         float s[2][C];
+        const f32x2 q_lo = pair(1.f / QLO, 1.f / QLO);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const f32x2 kf = pair(ke[h] << 23, ke[h] << 23);
@@ -994,10 +998,10 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
             const float4 f4 = *reinterpret_cast<const float4*>(&m.qf[wg * C + c]);
-            unpair(mul2(add2(pair(hi[c], hi[c + 1]), pair(lo[c], lo[c + 1])),
+            unpair(mul2(fma2(pair(lo[c], lo[c + 1]), q_lo, pair(hi[c], hi[c + 1])),
                         mul2(pair(f4.x, f4.y), kf)),
                    s[h][c], s[h][c + 1]);
-            unpair(mul2(add2(pair(hi[c + 2], hi[c + 3]), pair(lo[c + 2], lo[c + 3])),
+            unpair(mul2(fma2(pair(lo[c + 2], lo[c + 3]), q_lo, pair(hi[c + 2], hi[c + 3])),
                         mul2(pair(f4.z, f4.w), kf)),
                    s[h][c + 2], s[h][c + 3]);
           }

@@ -130,3 +130,24 @@ def test_values_of_every_magnitude(dev):
     out = run_attention(a, parent, q, dev)
     assert_device_ok()
     check_bars(a, parent, q, out, dev)
+
+
+@pytest.mark.parametrize("ratio", [0, 8, 11, 13, 16])
+@pytest.mark.parametrize("D,Hq", [(64, 16), (128, 6)])
+def test_a_large_query_channel_leaves_the_others_their_precision(D, Hq, ratio, dev):
+    """Queries with one channel 2^ratio above the others where K is zero, and the others
+    scaled so that the scores are as spread as ever."""
+    rng = np.random.default_rng(330 + ratio)
+    a = Setup(rng, dev, [600, 90], None, 2, 2, D, 32)
+    a.cache["k"][:, :, :, 5] = 0
+    a.upload(dev)
+    q = rng.standard_normal((2, 2, Hq, D)) * 2.0 ** -ratio
+    q[..., 5] = 3.7
+    q = bf16_bits(q.astype(np.float32))
+    scale = 2.0 ** (ratio - 3)
+    out = run_attention(a, None, q, dev, scale)
+    assert_device_ok()
+    got, ref = bf16_to_f64(bf16_host(out)), osp.tree_attention(a.cache, a.table, a.pos, None, None,
+                                                               q, scale)
+    assert np.linalg.norm(got - ref) <= (2.0 ** -8 + 2.0 ** -9) * np.linalg.norm(ref)
+    check_bars(a, None, q, out, dev, scale)

@@ -11,7 +11,7 @@ v_t = code_t * 2^(e_t), the output o = sum p_t v_t:
     is scaled to 224 .. 448, and half of e4m3's smallest step is 2^-10, so a weight is
     off by up to 2^-10 / 224 (2^-17.8) of that, times |code_t|;
   * a score's error ds_t, fp32 sums of D products (D 2^-24 sum |q k|) and the values of
-    q that are no multiple of 2^-9 of the row's scale, off by half of that: p_t ds_t
+    q that are no multiple of 2^-13 of the row's scale, off by half of that: p_t ds_t
     |v_t| and, through the sum of the weights, max ds_t |o|;
   * fp32 sums over the tiles and the exponential (2^-22): 2^-19 of sum p_t |v_t|.
 `bound` is the sum of these for every value: no result of the formula may exceed it.
@@ -87,8 +87,8 @@ class Bars:
                 o = w @ v
                 # q in units of its row's scale: the smallest 2^e with max|q| <= 448 2^e
                 e = torch.ceil(torch.log2(x.abs().amax(-1, keepdim=True).clamp(min=1e-300) / 448))
-                u = x / torch.exp2(e) * 512
-                dq = torch.where(u == torch.round(u), 0.0, torch.exp2(e - 10))
+                u = x / torch.exp2(e) * 2.0 ** 13
+                dq = torch.where(u == torch.round(u), 0.0, torch.exp2(e - 14))
                 ds = sc * (dq @ k.abs().T + D * 2.0 ** -24 * (x.abs() @ k.abs().T))
                 ds_top = torch.where(vis, ds, 0.0).amax(-1, keepdim=True)
                 a = 2.0 ** -9 + 2.0 ** -11
