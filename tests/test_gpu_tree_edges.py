@@ -151,3 +151,21 @@ def test_a_large_query_channel_leaves_the_others_their_precision(D, Hq, ratio, d
                                                                q, scale)
     assert np.linalg.norm(got - ref) <= (2.0 ** -8 + 2.0 ** -9) * np.linalg.norm(ref)
     check_bars(a, None, q, out, dev, scale)
+
+
+@pytest.mark.parametrize("ratio", [0, 4, 8, 12, 15])
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 24)])
+def test_scores_that_differ_little_from_a_large_common_part(D, Hq, ratio, dev):
+    """A channel with the same large K at every position: the sums of products keep what
+    the other channels add to it."""
+    rng = np.random.default_rng(340 + ratio)
+    a = Setup(rng, dev, [520, 33], None, 3, 2, D, 64)
+    a.cache["k"][:, :, :, 9] = 0x7E                      # 448, the others below 256
+    a.cache["k_exp"][:] = 127 - 8
+    a.upload(dev)
+    q = rng.standard_normal((2, 3, Hq, D))
+    q[..., 9] = 0.83 * 2.0 ** ratio
+    q = bf16_bits(q.astype(np.float32))
+    out = run_attention(a, None, q, dev)
+    assert_device_ok()
+    check_bars(a, None, q, out, dev)
