@@ -39,11 +39,12 @@ def _seen(parent, n, dev):
 
 class Bars:
     """ref, bound [B][N][Hq][D] and row [B][N][Hq], NaN for slots behind the counts;
-    the cache's rows that are seen must hold no NaN.  `drop` [B] -> positions that are
-    left out, `twice` [B] -> positions that count twice (to see that the bars notice)."""
+    the cache's rows that are seen must hold no NaN.  `only`: the sequences to look at,
+    the others stay NaN.  `drop` {b: positions that are left out}, `twice` {b: positions
+    that count twice}: wrong results, to see that the bars notice."""
 
-    def __init__(self, cache, table, pos, count, parent, q, scale=None, dev="cpu", drop=None,
-                 twice=None):
+    def __init__(self, cache, table, pos, count, parent, q, scale=None, dev="cpu", only=None,
+                 drop=None, twice=None):
         t = {n: torch.as_tensor(x).to(dev) for n, x in cache.items()}
         pages, Hkv, page, D = t["k"].shape
         B, N, Hq, _ = q.shape
@@ -56,12 +57,15 @@ class Bars:
         self.ref = torch.full((B, N, Hq, D), float("nan"), **f64)
         self.bound, self.row = self.ref.clone(), torch.full((B, N, Hq), float("nan"), **f64)
         for b, p, n in osp._ranges(table, pos, count, N):
-            if n == 0:
+            if n == 0 or (only is not None and b not in only):
                 continue
             at = torch.arange(min(p + n, tab.shape[1] * page), device=dev)
             pg = tab[b, at // page]
             good = (pg >= 0) & (pg < pages)
             at, pg = at[good], pg[good]
+            if len(at) == 0:                 # a sequence without a valid page
+                self.ref[b, :n] = self.bound[b, :n] = self.row[b, :n] = 0.0
+                continue
             node = at - p
             sees = torch.ones((n, len(at)), dtype=torch.bool, device=dev)
             late = node >= 0
