@@ -1391,9 +1391,13 @@ static cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const C
   const int grid = tree_ctas(sm_count());
   e = launch_in_order(tree_attn_kernel<D, R>, grid, F::THREADS, SMEM, stream, 0, mk, mv, a);
   if (e != cudaSuccess) return e;
-  // many parts per unit: a row's parts over 8 warps; few: a row per warp
+  // Many parts per unit: a row's parts over 8 warps; few: a row per warp.  The whole
+  // call with 4 KV heads of 4 nodes, over 8 warps and one: behind 34,000 positions 4 units
+  // 21.4 and 33.4 us, 16 31.9 and 33.7, 24 35.6 and 36.5, 28 40.2 and 39.6, 36 49.3 and
+  // 47.1, 72 77.3 and 69.2; behind 3,000 or fewer 4 to 20 units 13.9 to 20.2 and 17.6 to
+  // 21.5, 36 19.0 and 16.5, 72 26.3 and 19.1.
   const int units = a.s.B * a.c.Hkv * a.blocks;
-  const bool wide = grid / units >= 4;
+  const bool wide = grid / units >= 12;
   return launch_in_order(
       wide ? tree_attn_combine_kernel<D, R, 8> : tree_attn_combine_kernel<D, R, 1>,
       dim3(units, wide ? R : R / 8), 256, 0, stream, 0, a);
