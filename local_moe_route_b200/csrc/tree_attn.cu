@@ -89,7 +89,12 @@ constexpr float QLO = 16.f;                 // the low parts of q are held times
 constexpr int SPREAD = 30;
 // What a unit costs besides its tiles (its query rows, the tree's masks, its
 // results), in tiles: units take that much more of the line.  On short lines
-// the number of tiles per CTA counts, not their even cost.
+// the number of tiles per CTA counts, not their even cost.  With a cost of 0, 1, 2
+// and 3: 8 tiles 10.2, 12.5, 11.4, 12.5 us; 8 nodes of 12 short sequences (0.8 tiles
+// per CTA) 14.7, 16.4, 17.5, 18.4; 4 nodes behind 34,000 (1.8 per CTA) 24.1, 21.4, 21.3,
+// 21.3; 24 sequences to 3,000 (2 per CTA) 25.3, 22.9, 22.1, 23.3, but 9 of them (just
+// above 1) 16.5 with 1 and 17.1 with 2; 24-node trees of 16 (10 per CTA) 52.5, 46.5, 45.7,
+// 46.3; 32 sequences to 34,000 (30 per CTA) 116.9, 111.8, 109.9, 108.0.
 __host__ __device__ constexpr uint32_t unit_cost(uint32_t tiles, uint32_t ctas) {
   return tiles >= 16 * ctas ? 3 : tiles >= 4 * ctas ? 2 : tiles > ctas ? 1 : 0;
 }
