@@ -33,9 +33,10 @@
 // a position adds to the output, score and V scale together, per row and tile: a
 // large V that a row gives no weight to, or that another node sees, takes nothing
 // from the others, and positions of a tile far below an earlier tile's maximum keep
-// their precision.  The sum of the softmax comes from s alone, scaled to the same
-// r less the tile's largest exponent where its exponents lie close together, to its
-// own maximum (a third barrier) where they do not, e.g. beside a V row of zeros.
+// their precision.  ev enters with the multiplication by the K factor, so the weight
+// is one exponential and the softmax's sum takes it times 2^(largest ev - ev), a factor
+// per position.  Where a tile's exponents lie too far apart for that, e.g. beside a V
+// row of zeros, the sum has a reference and exponentials of its own (a third barrier).
 // References are integers (log2 domain), so rescaling is an exponent addition.
 //
 // Work: the tiles (256 positions) of all (sequence, KV head, block of R rows)
@@ -82,10 +83,10 @@ namespace ta {
 constexpr int SUB = 128;                    // positions per MMA tile
 constexpr int TILE = 2 * SUB;               // positions per softmax step
 constexpr int NODES = STRATA_TREE_MAX_NODES;
-constexpr float WSCALE = 448.f;             // weights are scaled to e4m3's largest value
+constexpr float LOG2_WSCALE = 8.807354922f; // weights are scaled to e4m3's largest value, 448
 constexpr float QLO = 16.f;                 // the low parts of q are held times this
-// V exponents of a tile that lie no further apart share one reference for the scores
-// and the weights (the sums then hold up to 2^SPREAD times the weights).
+// V exponents of a tile that lie no further apart: the scores need no reference of
+// their own (the sums then hold up to 2^SPREAD times the weights).
 constexpr int SPREAD = 30;
 // What a unit costs besides its tiles (its query rows, the tree's masks, its
 // results), in tiles: units take that much more of the line.  On short lines
@@ -156,9 +157,9 @@ struct Misc {
   uint2 wexp[F::NWG][4];      // per warp: largest V exponent that a row sees; 255 - the smallest
   alignas(16) float mref[F::NWG][C], beta[F::NWG][C], alpha[F::NWG][C];
   alignas(16) float beta_o[F::NWG][2][C];
-  alignas(16) float eh[F::NWG][C];            // per row: 2^-(the scale of its weights)
+  alignas(16) float sref[F::NWG][C];          // mref of the scores, where they have their own
   alignas(16) float lsum[F::NWG][4][C];       // per warp: sums of the weights
-  alignas(16) float inv[R];                   // 1 / (sum * WSCALE)
+  alignas(16) float inv[R];                   // 1 / sum
 };
 
 __host__ __device__ constexpr size_t slot_floats(int R, int D) { return (size_t)R * (D + 2); }
@@ -993,21 +994,22 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
         }
         ok = ta_wait(&m.s_full, g & 1, abort_flag, a.err) && ok;
         tc_fence_after();
-        float s[2][C];
+        float s[2][C];                       // score plus V exponent
         const f32x2 q_lo = pair(1.f / QLO, 1.f / QLO);
+        const float ev[2] = {(float)((int)ve[0] - 127), (float)((int)ve[1] - 127)};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const f32x2 kf = pair(ke[h] << 23, ke[h] << 23);
+          const f32x2 kf = pair(ke[h] << 23, ke[h] << 23), e2 = pair(ev[h], ev[h]);
           uint32_t hi[C], lo[C];
           tmem_load2(lanes_at + h * 2 * R, lanes_at + h * 2 * R + R, hi, lo);
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
             const float4 f4 = *reinterpret_cast<const float4*>(&m.qf[wg * C + c]);
-            unpair(mul2(fma2(pair(lo[c], lo[c + 1]), q_lo, pair(hi[c], hi[c + 1])),
-                        mul2(pair(f4.x, f4.y), kf)),
+            unpair(fma2(fma2(pair(lo[c], lo[c + 1]), q_lo, pair(hi[c], hi[c + 1])),
+                        mul2(pair(f4.x, f4.y), kf), e2),
                    s[h][c], s[h][c + 1]);
-            unpair(mul2(fma2(pair(lo[c + 2], lo[c + 3]), q_lo, pair(hi[c + 2], hi[c + 3])),
-                        mul2(pair(f4.z, f4.w), kf)),
+            unpair(fma2(fma2(pair(lo[c + 2], lo[c + 3]), q_lo, pair(hi[c + 2], hi[c + 3])),
+                        mul2(pair(f4.z, f4.w), kf), e2),
                    s[h][c + 2], s[h][c + 3]);
           }
         }
@@ -1021,18 +1023,10 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
               if (!((vis[h] >> c) & 1)) s[h][c] = -INFINITY;
           }
         }
-        const float ev[2] = {(float)((int)ve[0] - 127), (float)((int)ve[1] - 127)};
         {
-          const f32x2 e0 = pair(ev[0], ev[0]), e1 = pair(ev[1], ev[1]);
           float w[C];
 #pragma unroll
-          for (int c = 0; c < C; c += 2) {
-            float x0, x1, y0, y1;
-            unpair(add2(pair(s[0][c], s[0][c + 1]), e0), x0, x1);
-            unpair(add2(pair(s[1][c], s[1][c + 1]), e1), y0, y1);
-            w[c] = warp_max(fmaxf(x0, y0));
-            w[c + 1] = warp_max(fmaxf(x1, y1));
-          }
+          for (int c = 0; c < C; ++c) w[c] = warp_max(fmaxf(s[0][c], s[1][c]));
           if (lane == 0) {
 #pragma unroll
             for (int c = 0; c < C; c += 4)
@@ -1058,7 +1052,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
         if (per_row) {
 #pragma unroll
           for (int c = 0; c < C; ++c) {
-            const float w = warp_max(fmaxf(s[0][c], s[1][c]));
+            const float w = warp_max(fmaxf(s[0][c] - ev[0], s[1][c] - ev[1]));
             if (lane == 0) m.wscore[wg][wq][c] = w;
           }
           named_barrier_sync(bar_wg, 128);
@@ -1067,7 +1061,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
         if (lt < C) {
           const float top = fmaxf(fmaxf(m.wmax[wg][0][lt], m.wmax[wg][1][lt]),
                                   fmaxf(m.wmax[wg][2][lt], m.wmax[wg][3][lt]));
-          // the reference of the row's scores, and of its weights above that
+          // the reference of the row's scores, and that of its weights above it
           float ref = ceilf(top) - (float)(etop - 127);
           int lift = etop - 127;
           if (per_row) {
@@ -1075,11 +1069,10 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
                               fmaxf(m.wscore[wg][2][lt], m.wscore[wg][3][lt])));
             lift = min(max((int)(ceilf(top) - ref), -127), 127);
           }
-          // 2^-lift; 2^-127 is subnormal
-          m.eh[wg][lt] = lift < 127 ? __uint_as_float((uint32_t)(127 - lift) << 23)
-                                    : __uint_as_float(1u << 22);
           // a tile without a visible position changes nothing
           if (top == -INFINITY) ref = m_run == -INFINITY ? 0.f : m_run;
+          m.mref[wg][lt] = LOG2_WSCALE - (top == -INFINITY ? 0.f : ceilf(top));
+          m.sref[wg][lt] = LOG2_WSCALE - ref;
           const float now = top == -INFINITY ? m_run : fmaxf(m_run, ref);
           float al = 1.f;
           if (now != m_run) {
@@ -1088,7 +1081,6 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
           }
           const int d = now == -INFINITY ? 0 : (int)fmaxf(ref - now, -200.f);
           m_run = now;
-          m.mref[wg][lt] = -ref;
           m.alpha[wg][lt] = al;
           m.beta[wg][lt] = pow2i(d);
           m.beta_o[wg][g & 1][lt] = pow2i(d + lift);
@@ -1104,6 +1096,28 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
             l[c / 2] = mul2(l[c / 2], pair(a4.x, a4.y));
             l[c / 2 + 1] = mul2(l[c / 2 + 1], pair(a4.z, a4.w));
           }
+        }
+        if (per_row) {
+#pragma unroll
+          for (int c = 0; c < C; c += 2) {
+            const float r0 = m.sref[wg][c], r1 = m.sref[wg][c + 1];
+            f32x2 p[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              p[h] = pair(ta_exp2((s[h][c] - ev[h]) + r0), ta_exp2((s[h][c + 1] - ev[h]) + r1));
+            l[c / 2] = fma2(add2(p[0], p[1]), pair(m.beta[wg][c], m.beta[wg][c + 1]), l[c / 2]);
+          }
+        }
+        // The weights go to the codes as they are (with the scale and the rounding to fp16
+        // in a pass of their own 24-node trees took 46.1 us for 44.3); the softmax's own,
+        // whose sum the row is divided by, are these times 2^(lift - ev).
+        uint32_t ph[2][C / 2];
+        f32x2 back[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // (bounded where the weight is 0 and the exponent any)
+          const int up = min(max(etop - (int)ve[h], -126), SPREAD) + 127;
+          back[h] = pair((uint32_t)up << 23, (uint32_t)up << 23);
         }
 #pragma unroll
         for (int c = 0; c < C; c += 4) {
@@ -1121,33 +1135,10 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
               x = ta_exp2(x);
               y = ta_exp2(y);
               p[h] = pair(x, y);
-              s[h][c + 2 * j] = x;
-              s[h][c + 2 * j + 1] = y;
+              ph[h][c / 2 + j] = pack_f16x2(x, y);
             }
-            l[c / 2 + j] = fma2(add2(p[0], p[1]), bb[j], l[c / 2 + j]);
-          }
-        }
-        // with the position's V scale, in fp16
-        uint32_t ph[2][C / 2];
-        float vf[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // 2^(ev - lift).  Beyond the bounds only where the weight is 0: in the common
-          // case lift is the largest exponent, else weight and factor have a product
-          // of 1 at most, and the weight is 2^-126 at least
-          const float f = __uint_as_float(ve[h] << 23);
-          if (per_row) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) s[h][c] *= fminf(f * m.eh[wg][c], 0x1p126f);
-            vf[h] = WSCALE;
-          } else {
-            vf[h] = fminf(f * m.eh[wg][0], 1.f) * WSCALE;
-          }
-#pragma unroll
-          for (int c = 0; c < C; c += 2) {
-            float x, y;
-            unpair(mul2(pair(s[h][c], s[h][c + 1]), pair(vf[h], vf[h])), x, y);
-            ph[h][c / 2] = pack_f16x2(x, y);
+            if (!per_row)
+              l[c / 2 + j] = fma2(fma2(p[0], back[0], mul2(p[1], back[1])), bb[j], l[c / 2 + j]);
           }
         }
         // the tile before: its output, now that its product is done
@@ -1237,7 +1228,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
                       (m.lsum[wg][2][lt] + m.lsum[wg][3][lt]);
           // (its scores are 0: without a position it sees nothing was added)
           if (m.nan_row[r] && sum != 0.f) sum = __uint_as_float(0x7FC00000u);
-          m.inv[r] = sum == 0.f ? 0.f : 1.f / (sum * WSCALE);
+          m.inv[r] = sum == 0.f ? 0.f : 1.f / sum;
           if (!whole) {
             float* part =
                 a.parts + (size_t)(2 * u.run + (u.first == 0)) * slot_floats(R, D) + R * D + 2 * r;
@@ -1351,7 +1342,7 @@ __global__ void __launch_bounds__(256) tree_attn_combine_kernel(const TreeArgs a
     }
   }
   if (node >= t.count) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / (sum * WSCALE);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint16_t* dst = a.out + (((int64_t)b * a.s.N + node) * a.Hq + h) * D + lane * V;
 #pragma unroll
   for (int j = 0; j < V; j += 2)
