@@ -42,8 +42,10 @@ extern "C" {
  *            are NaN)
  *   k_exp, v_exp [pages][Hkv][page] exponents, biased by 127
  * A row (one position of one head, K or V) stands for the values
- * code * 2^(exp - 127).  A row whose exponent byte is 0 holds nothing:
- * attention passes over it, strata_kv_read gives zeros for it.
+ * code * 2^(exp - 127); strata_kv_append writes exponents of 1 .. 246.  A row whose
+ * exponent byte is 0 holds nothing: attention passes over it (over V alone when K is
+ * held: the position keeps its weight), strata_kv_read gives zeros for it.  A byte of
+ * 255 is not to be used.
  * pages * Hkv * page < 2^31. */
 typedef struct {
   int32_t pages, page, Hkv, D;
@@ -177,6 +179,7 @@ STRATA_API strata_status_t strata_verify_drafts(const int32_t* tokens, const int
  * for i < path_len[b], all of them as they were before the call.
  *   path     [B][N] int32 (N <= STRATA_TREE_MAX_NODES), as strata_verify_drafts
  *            writes it; an entry outside [i, N) is reported and its row not moved
+ *            (pos_out counts it all the same: what position pos[b] + i held stays)
  *   path_len [B] int32; outside 0 .. N is reported and counts as 0
  *   pos_out  [B] int32 out: pos[b] + path_len[b]; may be pos itself
  * seqs.count is not used; B <= 65535. */

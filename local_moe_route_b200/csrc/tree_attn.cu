@@ -54,19 +54,19 @@
 //
 // R, the rows per block, is 16 when all rows of N nodes fit and 32 otherwise,
 // with two CTAs per SM (their TMEM and registers).  Blocks of 64 rows (one CTA per
-// SM) were 5 % faster on 64-node trees of 4 sequences (72 against 75 us) and 10 to
-// 20 % slower on 8-node and on few trees; blocks of 16 for all rows 36 % slower on
-// 24-node trees.
+// SM) were 5 % faster on 64-node trees of 4 sequences and 10 to 20 % slower on 8-node
+// and on few trees; blocks of 16 for all rows 36 % slower on 24-node trees.
 //
-// Measured (D = 128, 4 KV heads, 32 query heads, one call, burst clocks): 32
-// sequences of 4 nodes behind up to 34,000 positions 105 us, 5.5 TB/s of the
-// cache's bytes (0.84 of the copy rate; the same with one node 97 us); one
-// sequence behind 34,000 21 us; one token behind 300 positions 10 us, of which 2 us
-// are the launch, 6 us the first tile's chain of dependent steps (lengths -> page
-// -> copy -> scores) and 2 us the join.  In a long line a tile takes a CTA
-// 3.3 us, with two CTAs per SM near what its 66 KB take at the copy rate; D = 64
-// halves the bytes but not the arithmetic (98 us): the softmax warps then issue
-// about half of the time and wait for each other the rest.  Steps that did not
+// Measured (D = 128, 4 KV heads, 32 query heads, one call): 32 sequences of 4 nodes
+// behind up to 34,000 positions 106 us in a graph at burst clocks, 5.5 TB/s of the
+// cache's bytes (0.83 of the copy rate; with one node 98 us), 128 us called without a
+// pause (4.5 TB/s, 0.69: the clock falls to 1.66 GHz); one sequence behind 34,000
+// 21 us; one token behind 300 positions 10 us, of which 2 us are the launch, 6 us the
+// first tile's chain of dependent steps (lengths -> page -> copy -> scores) and 2 us
+// the join.  In a long line a tile takes a CTA 3.3 us, with two CTAs per SM near what
+// its 66 KB take at the copy rate; D = 64 halves the bytes but not the arithmetic
+// (97 us): 25 to 27 instructions a weight, issued in about half of the cycles, the
+// softmax warps waiting for tensor memory and for each other the rest.  Steps that did not
 // help: the last fifth of the line in small runs taken from a counter (141 us
 // against 126: a run costs two tiles), one barrier per tile with every warp
 // working out the references (112 against 108), 8 columns per warpgroup.
