@@ -87,22 +87,16 @@ def _rows(t: Any, dev: int, B: int, N: int, heads: int, D: int):
     return t.data_ptr(), step
 
 
-def _step(given: int, own: int, dense: int, *rows: Any) -> int:
-    """The token stride of a call: that of tensors that are parts of wider rows, or the
-    one given with raw pointers.  Beside a dense tensor any other than its own would
-    lead past its end."""
-    if own:
-        return own
-    if given and given != dense and any(t is not None and t.__class__ is not int for t in rows):
+def _step(given: int, dense: int, *rows: Any) -> int:
+    """The token stride given with raw pointers.  Beside a dense tensor any other than
+    its own would lead past its end."""
+    if given != dense and any(t is not None and t.__class__ is not int for t in rows):
         raise _Refused
     return given
 
 
-def _ws_bytes(ws: Any, given: Optional[int]) -> int:
-    """Size of the workspace: what is given with a raw pointer, and no more than a
-    tensor has."""
-    if given is None:
-        return _nbytes(ws)
+def _ws_bytes(ws: Any, given: int) -> int:
+    """The workspace's size as it is given, and no more than a tensor has."""
     n = max(int(given), 0)               # (it travels as a size without a sign)
     return n if ws is None or ws.__class__ is int else min(n, _nbytes(ws))
 
@@ -213,7 +207,7 @@ def strata_kv_append(cache: KvCache, seqs: KvSeqs, k, v, stride: int = 0, stream
         vp, vs = _rows(v, dev, seqs.B, seqs.N, cache.Hkv, cache.D)
         if ks != vs:
             raise _Refused
-        step = _step(stride, ks, cache.Hkv * cache.D, k, v)
+        step = ks or stride and _step(stride, cache.Hkv * cache.D, k, v)
     except _Refused:
         return STRATA_ERR_INVALID_ARG
     return (_bound or _lib()).strata_kv_append(cache, seqs, kp, vp, step, _on(stream, dev))
@@ -268,14 +262,14 @@ def strata_tree_attention(cache: KvCache, seqs: KvSeqs, parent, q, scale, out, w
             Hq = q.shape[2] if q.dim() == 4 else 0
         heads = int(Hq or 0)
         qp, qs = _rows(q, dev, B, N, heads, D)
-        step = _step(q_stride, qs, heads * D, q)
+        step = qs or q_stride and _step(q_stride, heads * D, q)
         op, pp = _dev(out, _bf16, dev, B * N * heads * D), _dev(parent, _i32, dev, B * N)
         wp = _dev(ws, _u8, dev)
     except _Refused:
         return STRATA_ERR_INVALID_ARG
     return (_bound or _lib()).strata_tree_attention(
         cache, seqs, pp, qp, step, heads, scale, op, wp,
-        _ws_bytes(ws, ws_bytes), _on(stream, dev))
+        _nbytes(ws) if ws_bytes is None else _ws_bytes(ws, ws_bytes), _on(stream, dev))
 
 
 def strata_verify_drafts(tokens, parent, count, p, q, u_accept, u_sample, dims, path, path_len,
