@@ -58,9 +58,9 @@
 // and on few trees; blocks of 16 for all rows 36 % slower on 24-node trees.
 //
 // Measured (D = 128, 4 KV heads, 32 query heads, one call): 32 sequences of 4 nodes
-// behind up to 34,000 positions 106 us in a graph at burst clocks, 5.5 TB/s of the
-// cache's bytes (0.83 of the copy rate; with one node 98 us), 128 us called without a
-// pause (4.5 TB/s, 0.69: the clock falls to 1.66 GHz); one sequence behind 34,000
+// behind up to 34,000 positions 105 us in a graph at burst clocks, 5.5 TB/s of the
+// cache's bytes (0.84 of the copy rate; with one node 98 us), 125 us called without a
+// pause (4.7 TB/s, 0.71: the clock falls to 1.66 GHz); one sequence behind 34,000
 // 21 us; one token behind 300 positions 10 us, of which 2 us are the launch, 6 us the
 // first tile's chain of dependent steps (lengths -> page -> copy -> scores) and 2 us
 // the join.  In a long line a tile takes a CTA 3.3 us, with two CTAs per SM near what
@@ -1049,10 +1049,13 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
         elow = 255 - elow;
         // Far apart, and the scores need a maximum of their own
         const bool per_row = etop - elow > SPREAD;
+        // (The exponents are read again where the scores are wanted without them: kept in
+        // registers they cost 32 long sequences 106.4 us for 105.1.)
+        auto exponent = [&](int h) { return (float)((int)e[TILE + h * SUB] - 127); };
         if (per_row) {
 #pragma unroll
           for (int c = 0; c < C; ++c) {
-            const float w = warp_max(fmaxf(s[0][c] - ev[0], s[1][c] - ev[1]));
+            const float w = warp_max(fmaxf(s[0][c] - exponent(0), s[1][c] - exponent(1)));
             if (lane == 0) m.wscore[wg][wq][c] = w;
           }
           named_barrier_sync(bar_wg, 128);
@@ -1104,7 +1107,8 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
             f32x2 p[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              p[h] = pair(ta_exp2((s[h][c] - ev[h]) + r0), ta_exp2((s[h][c + 1] - ev[h]) + r1));
+              p[h] = pair(ta_exp2((s[h][c] - exponent(h)) + r0),
+                          ta_exp2((s[h][c + 1] - exponent(h)) + r1));
             l[c / 2] = fma2(add2(p[0], p[1]), pair(m.beta[wg][c], m.beta[wg][c + 1]), l[c / 2]);
           }
         }
