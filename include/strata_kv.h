@@ -118,10 +118,11 @@ STRATA_API strata_status_t strata_kv_read(strata_kv_cache_t cache, strata_kv_seq
  * The sums over the positions hold 448 times the weights and V: with |V| up to
  * 2^87 they stay finite at any length, up to 2^103 at 32,768 positions.
  * Scores, softmax and sums in fp32 (values of q below 2^-13.8 of their row's largest
- * are rounded to 2^-21.8 of it, all others taken as they are); for the product with V what a position adds to
- * a row (its weight times 2^(v_exp - 127)) is rounded to 2^-9 of its value, or to
- * 2^-17.8 of the row's largest in the same tile of 256 positions where that is
- * more: a large V without weight takes nothing from the others.
+ * are rounded to 2^-21.8 of it, all others taken as they are); for the product with
+ * V what a position adds to a row (its weight times 2^(v_exp - 127)) is rounded to
+ * 2^-9 of its value, or to 2^-17.8 of the row's largest in the same tile of 256
+ * positions where that is more: a large V without weight takes nothing from the
+ * others.
  *   ws       scratch of strata_tree_attention_workspace_bytes() bytes, which
  *            reads the sizes of `cache` and `seqs` only (0 = refused) */
 STRATA_API size_t strata_tree_attention_workspace_bytes(strata_kv_cache_t cache,

@@ -1047,7 +1047,7 @@ __global__ void __launch_bounds__(ta::Cfg<D, R>::THREADS, ta::CTAS)
           elow = max(elow, (int)m.wexp[wg][i].y);
         }
         elow = 255 - elow;
-        // Far apart, and the scores need a maximum of their own
+        // V exponents too far apart: the scores need a maximum of their own
         const bool per_row = etop - elow > SPREAD;
         // (The exponents are read again where the scores are wanted without them: kept in
         // registers they cost 32 long sequences 106.4 us for 105.1.)

@@ -20,9 +20,9 @@
 // pass over 100,003 tokens of p and q takes about 4.2 us (2.7 us the sums, of which
 // 0.8 us are the conversions to 64 bits, 0.9 us the cluster's barrier); a greedy
 // chain of 3 drafts at 32,000 tokens takes 6.2 us in all, 32 trees of 16 nodes at
-// 100,003 tokens 24 to 31 us, by how many passes the longest of them needs.  Holding a node's rows in shared memory between its
-// passes was no faster (29.7 against 31.4 us then, and slower without
-// rejections), nor were 256 or 1024 threads.
+// 100,003 tokens 24 to 31 us, by how many passes the longest of them needs.
+// Holding a node's rows in shared memory between its passes was no faster (29.7
+// against 31.4 us then, and slower without rejections), nor were 256 or 1024 threads.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
